@@ -10,6 +10,7 @@
 
 #include "../../include/bitgemm.h"
 #include "bg_internal.h"
+#include "bg_kv.h"
 
 #define BG_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -589,6 +590,171 @@ BG_EXPORT int64_t gemm_w4a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M < 1 || M > kMaxM || N < 16 || N > kMaxRows || N % 16 || K < 256 || K > kMaxDim || K % 256) return 0;
     if (bg::w4a8_decode_fits(M, N, K)) return 0;
     return bg::w4a8_gemm_split(M, N, K).ws_bytes;
+}
+
+// ---- quantized KV cache ----
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int kMaxKvHeads = 1024;
+constexpr int64_t kMaxBatch = 65535;             // attention: grid.z
+
+// The cache descriptor of `fn`, checked.
+bg_status kv_cache_of(const char* fn, const bg_kv_cache* c, bg::KvCache* out) {
+    if (!c) return fail_in(fn, BG_ERR_NULL, "cache must be non-NULL");
+    if (!c->k || !c->v || !c->k_scales || !c->v_scales)
+        return fail_in(fn, BG_ERR_NULL, "the cache's k, v, k_scales and v_scales must be non-NULL");
+    if (c->format != BG_I8 && c->format != BG_FP8_E4M3 && c->format != BG_U4)
+        return fail_in(fn, BG_ERR_DTYPE, "cache format %lld is not I8/FP8_E4M3/U4", c->format);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail_in(fn, BG_ERR_SHAPE, "head_dim %lld is not 64, 128 or 256", c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > kMaxKvHeads)
+        return fail_in(fn, BG_ERR_SHAPE, "kv_heads %lld out of range", c->kv_heads);
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+        return fail_in(fn, BG_ERR_SHAPE, "page_size %lld is not a power of two in 16..1024", c->page_size);
+    if (c->pages < 1 || c->pages > INT32_MAX) return fail_in(fn, BG_ERR_SHAPE, "pages %lld out of range", c->pages);
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+        return fail_in(fn, BG_ERR_ALIGN, "the cache's buffers must be 16-byte aligned");
+    *out = bg::KvCache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), static_cast<uint32_t*>(c->k_scales),
+                       static_cast<uint32_t*>(c->v_scales), c->pages, __builtin_ctz((unsigned)c->page_size),
+                       c->kv_heads, c->head_dim, c->format};
+    return BG_OK;
+}
+
+// The sizes of p, checked; with `pointers`, what a launch reads too.
+bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool pointers, bg::KvAttnArgs* a) {
+    if (!p) return fail_in(fn, BG_ERR_NULL, "args must be non-NULL");
+    const bg_status st = kv_cache_of(fn, p->cache, &a->c);
+    if (st != BG_OK) return st;
+    if (p->dtype != BG_F16 && p->dtype != BG_BF16) return fail_in(fn, BG_ERR_DTYPE, "dtype %lld is not F16/BF16", p->dtype);
+    if (p->tokens < 0 || p->tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", p->tokens);
+    if (p->batch < 0 || p->batch > kMaxBatch) return fail_in(fn, BG_ERR_SHAPE, "batch=%lld out of range", p->batch);
+    if (p->q_heads < a->c.heads || p->q_heads > 16384 || p->q_heads % a->c.heads)
+        return fail_in(fn, BG_ERR_SHAPE, "q_heads=%lld is not a multiple of kv_heads=%lld", p->q_heads, a->c.heads);
+    if (p->max_pages < 1 || p->max_pages > INT32_MAX) return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld out of range", p->max_pages);
+    if (p->max_pages > (INT32_MAX >> a->c.page_shift))
+        return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld pages of %lld tokens pass 2^31 positions", p->max_pages, p->cache->page_size);
+    if (p->max_q < 1 || p->max_q > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "max_q=%lld out of range", p->max_q);
+    if (p->max_kv < 0) return fail_in(fn, BG_ERR_SHAPE, "max_kv=%lld is negative", p->max_kv);
+    if (p->window < 0 || p->sinks < 0) return fail_in(fn, BG_ERR_SHAPE, "window=%lld and sinks=%lld must not be negative", p->window, p->sinks);
+    if (p->q_token_stride % 8 || p->q_head_stride % 8)
+        return fail_in(fn, BG_ERR_ALIGN, "q strides %lld and %lld must be multiples of 8 elements", p->q_token_stride, p->q_head_stride);
+    if (!(p->scale > 0.0f) || p->scale > 3.0e38f) return fail_in(fn, BG_ERR_SHAPE, "scale must be positive and finite");
+    if (!p->cu_q && (p->tokens != p->batch || p->max_q != 1))
+        return fail_in(fn, BG_ERR_SHAPE, "without cu_q every sequence has one query: tokens=%lld, batch=%lld", p->tokens, p->batch);
+    if (tree && (p->tree_words < 1 || p->tree_words > 1024))
+        return fail_in(fn, BG_ERR_SHAPE, "tree_words=%lld out of range", p->tree_words);
+    if (tree && p->window) return fail_in(fn, BG_ERR_UNSUPPORTED, "a window of %lld with a tree", p->window);
+    if (pointers && p->tokens > 0 && p->batch > 0) {
+        if (!p->q || !p->out || !p->block_table || !p->kv_lens || (tree && !p->tree))
+            return fail_in(fn, BG_ERR_NULL, "q, out, block_table, kv_lens (and tree) must be non-NULL");
+        if (!aligned16(p->q) || !aligned16(p->out)) return fail_in(fn, BG_ERR_ALIGN, "q and out must be 16-byte aligned");
+        if ((reinterpret_cast<uintptr_t>(p->block_table) | reinterpret_cast<uintptr_t>(p->kv_lens) |
+             reinterpret_cast<uintptr_t>(p->cu_q) | reinterpret_cast<uintptr_t>(p->lse)) & 3u)
+            return fail_in(fn, BG_ERR_ALIGN, "block_table, kv_lens, cu_q and lse must be 4-byte aligned");
+        if (tree && (reinterpret_cast<uintptr_t>(p->tree) & 7u)) return fail_in(fn, BG_ERR_ALIGN, "tree must be 8-byte aligned");
+    }
+    a->q = p->q;
+    a->q_ts = p->q_token_stride;
+    a->q_hs = p->q_head_stride;
+    a->bf16 = p->dtype == BG_BF16;
+    a->tokens = p->tokens;
+    a->q_heads = p->q_heads;
+    a->table = p->block_table;
+    a->max_pages = p->max_pages;
+    a->kv_lens = p->kv_lens;
+    a->cu_q = p->cu_q;
+    a->batch = p->batch;
+    a->max_q = p->max_q < p->tokens ? p->max_q : p->tokens;
+    const int64_t room = p->max_pages << a->c.page_shift;
+    a->max_kv = p->max_kv == 0 || p->max_kv > room ? room : p->max_kv;
+    a->window = p->window > INT32_MAX ? 0 : p->window;   // positions stay below 2^31
+    a->sinks = a->window ? (p->sinks > INT32_MAX ? INT32_MAX : p->sinks) : 0;
+    a->tree = tree ? p->tree : nullptr;
+    a->tree_words = tree ? p->tree_words : 0;
+    a->scale = p->scale;
+    a->out = p->out;
+    a->lse = p->lse;
+    return BG_OK;
+}
+
+bg_status kv_attn_impl(const char* fn, const bg_kv_attn* p, bool tree, void* ws, int64_t ws_bytes, void* stream) {
+    bg::KvAttnArgs a{};
+    const bg_status st = kv_attn_args(fn, p, tree, true, &a);
+    if (st != BG_OK) return st;
+    if (a.tokens == 0 || a.batch == 0) {
+        g_last_error[0] = '\0';
+        return BG_OK;
+    }
+    const int64_t need = bg::kv_attn_workspace(a);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail_in(fn, BG_ERR_WORKSPACE, "workspace of %lld bytes needed (got %lld)", need, ws ? ws_bytes : 0);
+    if (ws && !aligned16(ws)) return fail_in(fn, BG_ERR_ALIGN, "the workspace must be 16-byte aligned");
+    note_kernel(bg::launch_kv_attn(a, ws, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+}  // namespace
+
+BG_EXPORT bg_status kv_cache_write(const bg_kv_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                   const void* v, int64_t v_token_stride, int64_t v_head_stride, int x_dtype,
+                                   const int64_t* slots, int64_t tokens, void* stream) {
+    const char* fn = "kv_cache_write";
+    bg::KvCache c;
+    const bg_status st = kv_cache_of(fn, cache, &c);
+    if (st != BG_OK) return st;
+    if (x_dtype != BG_F32 && x_dtype != BG_F16 && x_dtype != BG_BF16)
+        return fail_in(fn, BG_ERR_DTYPE, "x_dtype %lld is not F32/F16/BF16", x_dtype);
+    if (tokens < 0 || tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", tokens);
+    if (tokens == 0) {
+        g_last_error[0] = '\0';
+        return BG_OK;
+    }
+    if (!k || !v || !slots) return fail_in(fn, BG_ERR_NULL, "k, v and slots must be non-NULL");
+    const int64_t unit = x_dtype == BG_F32 ? 4 : 8;   // elements in 16 bytes
+    if (k_token_stride % unit || k_head_stride % unit || v_token_stride % unit || v_head_stride % unit)
+        return fail_in(fn, BG_ERR_ALIGN, "strides must be multiples of 16 bytes (%lld elements)", unit);
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return fail_in(fn, BG_ERR_ALIGN, "k and v must be 16-byte aligned, slots 8-byte aligned");
+    const bg::KvRows x{k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+    note_kernel(bg::launch_kv_write(c, x, x_dtype, tokens, slots, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+BG_EXPORT bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                                  int out_dtype, void* stream) {
+    const char* fn = "kv_cache_read";
+    bg::KvCache c;
+    const bg_status st = kv_cache_of(fn, cache, &c);
+    if (st != BG_OK) return st;
+    if (out_dtype != BG_F32 && out_dtype != BG_F16 && out_dtype != BG_BF16)
+        return fail_in(fn, BG_ERR_DTYPE, "out_dtype %lld is not F32/F16/BF16", out_dtype);
+    if (tokens < 0 || tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", tokens);
+    if (tokens == 0) {
+        g_last_error[0] = '\0';
+        return BG_OK;
+    }
+    if (!k || !v || !slots) return fail_in(fn, BG_ERR_NULL, "k, v and slots must be non-NULL");
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return fail_in(fn, BG_ERR_ALIGN, "k and v must be 16-byte aligned, slots 8-byte aligned");
+    note_kernel(bg::launch_kv_read(c, slots, tokens, out_dtype, k, v, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+BG_EXPORT bg_status kv_attn(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream) {
+    return kv_attn_impl("kv_attn", args, false, workspace, workspace_bytes, stream);
+}
+
+BG_EXPORT bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream) {
+    return kv_attn_impl("kv_attn_tree", args, true, workspace, workspace_bytes, stream);
+}
+
+BG_EXPORT int64_t kv_attn_workspace_bytes(const bg_kv_attn* args) {
+    bg::KvAttnArgs a{};
+    if (kv_attn_args("kv_attn_workspace_bytes", args, args && args->tree_words > 0, false, &a) != BG_OK) return 0;
+    if (a.tokens == 0 || a.batch == 0) return 0;
+    return bg::kv_attn_workspace(a);
 }
 
 BG_EXPORT const char* bg_status_string(int status) {

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -18,7 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("BG_LIB_PATH") or os.path.join(_PKG, "libbitgemm.so")
 
 # enums of include/bitgemm.h
-F32, F16, BF16, I8, FP8_E4M3, I32 = 0, 1, 2, 3, 4, 5
+F32, F16, BF16, I8, FP8_E4M3, I32, U4 = 0, 1, 2, 3, 4, 5, 6
 GRAN_TENSOR, GRAN_ROW, GRAN_ROW_G128, GRAN_BLOCK128 = 0, 1, 2, 3
 ALGO_AUTO, ALGO_GEMV, ALGO_SKINNY, ALGO_TILED, ALGO_SPLITK, ALGO_MID = 0, 1, 2, 3, 4, 5
 PACK_FORMAT_VERSION = 1
@@ -29,6 +30,7 @@ EXPORTS = (
     "gemm_w8a8_outlier", "gemm_w8a8",
     "gemm_w8a8_ex", "gemm_w8a8_ws", "gemm_w8a8_workspace_bytes", "gemm_w4a8", "gemm_w4a8_ws", "gemm_w4a8_workspace_bytes",
     "gemm_w4a16_algo", "gemm_w8a8_algo",
+    "kv_cache_write", "kv_cache_read", "kv_attn", "kv_attn_tree", "kv_attn_workspace_bytes",
     "bg_status_string", "bg_last_error",
     "bg_pack_format_version", "bg_last_kernel",
 )
@@ -82,6 +84,11 @@ def lib() -> ctypes.CDLL:
             "gemm_w4a8_workspace_bytes": [I64, I64, I64],
             "gemm_w4a16_algo": [I64, I64, I64, I],
             "gemm_w8a8_algo": [I64, I64, I64, I],
+            "kv_cache_write": [P, P, I64, I64, P, I64, I64, I, P, I64, P],
+            "kv_cache_read": [P, P, I64, P, P, I, P],
+            "kv_attn": [P, P, I64, P],
+            "kv_attn_tree": [P, P, I64, P],
+            "kv_attn_workspace_bytes": [P],
             "bg_status_string": [I],
             "bg_last_error": [],
             "bg_pack_format_version": [],
@@ -465,3 +472,240 @@ def gemm_w4a8(a: torch.Tensor, a_scales: torch.Tensor, a_gran: int, packed: Pack
 
 def gemm_w8a8_algo(M: int, N: int, K: int, fp8: bool = False) -> int:
     return lib().gemm_w8a8_algo(M, N, K, FP8_E4M3 if fp8 else I8)
+
+
+# ----------------------------------------------------------- KV cache --------
+
+_KV_CACHE = struct.Struct("@PPPPqiiii")               # bg_kv_cache
+_KV_ATTN = struct.Struct("@PPqqPqPPPPPqqqqqqiiif")    # bg_kv_attn
+_KV_DIMS = (64, 128, 256)
+
+
+@dataclass(frozen=True)
+class KVCache:
+    """A paged key/value cache in 8 or 4 bits: codes [pages][kv_heads][page_size][D]
+    (int8 for I8, E4M3 bytes as uint8 for FP8_E4M3) or [...][D / 2] uint8 (U4,
+    element 2i in the low nibble), and one record per token and head
+    [pages][kv_heads][page_size]: a float32 scale, or for U4 a float16 pair
+    (scale, zero-point) in a last axis of 2.  Slot n is token n % page_size of
+    page n // page_size."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    format: int
+
+    def __post_init__(self):
+        if self.format not in (I8, FP8_E4M3, U4):
+            raise ValueError(f"KVCache: format must be I8, FP8_E4M3 or U4, got {self.format}")
+        code, tail = (torch.int8 if self.format == I8 else torch.uint8), ((2,) if self.format == U4 else ())
+        record = torch.float16 if self.format == U4 else torch.float32
+        if self.k.dim() != 4 or self.k.dtype != code or self.v.dtype != code or self.v.shape != self.k.shape:
+            raise ValueError(f"KVCache: k and v must be {code} [pages][kv_heads][page_size][bytes of a row]")
+        for t in (self.k_scales, self.v_scales):
+            if t.dtype != record or tuple(t.shape) != (*self.k.shape[:3], *tail):
+                raise ValueError(f"KVCache: scales must be {record} {(*self.k.shape[:3], *tail)}")
+        pages, heads, page, width = self.k.shape
+        dim = 2 * width if self.format == U4 else width
+        if dim not in _KV_DIMS or pages < 1 or heads < 1 or page < 16 or page > 1024 or page & (page - 1):
+            raise ValueError(f"KVCache: head size {dim} must be one of {_KV_DIMS}, page_size {page} a power of two in 16..1024")
+        tensors = (self.k, self.v, self.k_scales, self.v_scales)
+        if any(t.device != self.k.device for t in tensors):
+            raise ValueError("KVCache: the tensors must be on one device")
+        ptrs = [_ptr(t).value for t in tensors]
+        desc = ctypes.create_string_buffer(_KV_CACHE.pack(*ptrs, pages, page, heads, dim, self.format), _KV_CACHE.size)
+        for name, value in (("_desc", desc), ("address", ctypes.addressof(desc)), ("device", self.k.device),
+                            ("pages", pages), ("page_size", page), ("kv_heads", heads), ("head_dim", dim)):
+            object.__setattr__(self, name, value)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scales, self.v_scales))
+
+
+def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, format: int, device="cuda") -> KVCache:
+    """A cache of `pages` pages whose slots hold zeros."""
+    if format not in (I8, FP8_E4M3, U4):
+        raise ValueError(f"kv_cache: format must be I8, FP8_E4M3 or U4, got {format}")
+    shape, u4 = (pages, kv_heads, page_size), format == U4
+    codes = [torch.zeros((*shape, head_dim // 2 if u4 else head_dim), dtype=torch.int8 if format == I8 else torch.uint8,
+                         device=device) for _ in range(2)]
+    scales = [torch.zeros((*shape, 2), dtype=torch.float16, device=device) if u4
+              else torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales, format)
+
+
+def _on_device(fn: str, cache: KVCache, *tensors):
+    for t in tensors:
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"{fn}: operands must be on the cache's device {cache.device}, got {t.device}")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the cache is on {cache.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _on_stream(stream, tensors, call):
+    """call() with `stream` current, so what it allocates belongs to that stream;
+    the operands' memory is kept from reuse until the stream has passed."""
+    with torch.cuda.stream(stream):
+        r = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return r
+
+
+def _kv_slots(fn: str, slots: torch.Tensor) -> int:
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError(f"{fn}: slots must be a contiguous int64 vector")
+    return slots.shape[0]
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Tensor, stream=None) -> None:
+    """Quantize the keys and values of T new tokens ([T][kv_heads][D], the last
+    axis contiguous, the others of any stride that is a multiple of 16 bytes:
+    slices of a fused projection's rows need no copy) into cache slots int64 [T].
+    A slot outside the cache (-1) skips its token."""
+    fn = "kv_cache_write"
+    if stream is not None:
+        return _on_stream(stream, (k, v, slots, cache.k, cache.v, cache.k_scales, cache.v_scales),
+                          lambda: kv_cache_write(k, v, cache, slots))
+    T = _kv_slots(fn, slots)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"{fn}: k {tuple(k.shape)} and v {tuple(v.shape)} must be {shape}")
+    dt = _TORCH_DT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise ValueError(f"{fn}: k and v must be of one type, float32, float16 or bfloat16 (got {k.dtype}, {v.dtype})")
+    if T == 0:
+        return
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError(f"{fn}: the last axis of k and v must be contiguous")
+    _on_device(fn, cache, k, v, slots)
+    _check(lib().kv_cache_write(cache.address, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt,
+                                slots.data_ptr(), T, torch.cuda.current_stream().cuda_stream), fn)
+
+
+def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """-> (k, v) of `dtype` [T][kv_heads][D]: the values of slots int64 [T].  A
+    slot outside the cache reads as zeros."""
+    fn = "kv_cache_read"
+    if stream is not None:
+        return _on_stream(stream, (slots, cache.k, cache.v, cache.k_scales, cache.v_scales),
+                          lambda: kv_cache_read(cache, slots, dtype))
+    T = _kv_slots(fn, slots)
+    dt = _TORCH_DT.get(dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: unsupported dtype {dtype}")
+    _on_device(fn, cache, slots)
+    k, v = (torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device) for _ in range(2))
+    if T:
+        _check(lib().kv_cache_read(cache.address, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), dt,
+                                   torch.cuda.current_stream().cuda_stream), fn)
+    return k, v
+
+
+_kv_workspaces: dict = {}
+
+
+def _kv_workspace(nbytes: int, device, stream: int) -> torch.Tensor:
+    """A workspace of at least nbytes, cached per device and stream."""
+    key = (device.index, stream)
+    ws = _kv_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _retired.append(ws)       # HIP graphs captured earlier may still use it
+        ws = torch.empty(1 << (nbytes - 1).bit_length(), dtype=torch.uint8, device=device)
+        _kv_workspaces[key] = ws
+    return ws
+
+
+def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, window, sinks, scale, out, lse, ws):
+    if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"{fn}: q must be [T][q_heads][{cache.head_dim}] with a contiguous last axis, got {tuple(q.shape)}")
+    T, heads, dim = q.shape
+    dt = _TORCH_DT.get(q.dtype)
+    if dt not in (F16, BF16):
+        raise ValueError(f"{fn}: q must be float16/bfloat16, got {q.dtype}")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError(f"{fn}: block_table must be a contiguous int32 matrix [batch][pages of a sequence]")
+    B, max_pages = block_table.shape
+    if kv_lens.dtype != torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous():
+        raise ValueError(f"{fn}: kv_lens must be a contiguous int32 vector of {B}")
+    if cu_q is not None and (cu_q.dtype != torch.int32 or cu_q.shape != (B + 1,) or not cu_q.is_contiguous()):
+        raise ValueError(f"{fn}: cu_q must be a contiguous int32 vector of {B + 1}")
+    words = 0
+    if tree is not None:
+        if tree.dtype != torch.int64 or tree.dim() != 2 or tree.shape[0] != T or not tree.is_contiguous():
+            raise ValueError(f"{fn}: tree must be a contiguous int64 matrix [{T}][words]")
+        words = tree.shape[1]
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != (T, heads, dim) or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError(f"{fn}: out must be a contiguous {(T, heads, dim)} of {q.dtype}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
+        raise ValueError(f"{fn}: lse must be a contiguous float32 {(T, heads)}")
+    if T == 0 or B == 0:
+        return out
+    _on_device(fn, cache, q, block_table, kv_lens, cu_q, tree, out, lse, ws)
+    L = lib()
+    s = torch.cuda.current_stream().cuda_stream
+    args = _KV_ATTN.pack(
+        cache.address, q.data_ptr(), q.stride(0), q.stride(1), block_table.data_ptr(), max_pages, kv_lens.data_ptr(),
+        0 if cu_q is None else cu_q.data_ptr(), 0 if tree is None else tree.data_ptr(), out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), T, B, max_q_len, max_kv_len, window, sinks, heads, dt, words,
+        dim ** -0.5 if scale is None else scale)
+    if ws is None:
+        need = L.kv_attn_workspace_bytes(args)
+        ws = _kv_workspace(need, q.device, s) if need > 0 else None
+    elif not ws.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be contiguous")
+    _check(getattr(L, fn)(args, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), s), fn)
+    return out
+
+
+def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+            cu_q: torch.Tensor | None = None, max_q_len: int = 1, *, max_kv_len: int = 0, window: int = 0, sinks: int = 0,
+            scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+            ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of ragged queries [T][q_heads][D] over the cache -> [T][q_heads][D].
+
+    Sequence b owns the queries cu_q[b] .. cu_q[b + 1] - 1 (cu_q None: one query
+    per sequence), which are the last of its kv_lens[b] positions; position j
+    lies in page block_table[b][j // page_size] (a page outside the cache, such
+    as -1, holds nothing).  A query sees the positions up to its own; with a
+    window only the last `window` of them and the first `sinks`.  A query that
+    sees nothing gives zeros.  max_q_len and max_kv_len (0: the table's width)
+    are host-side bounds of the lengths.  scale None: D ** -0.5.  lse: float32
+    [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
+    workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream."""
+    if stream is not None:
+        return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, out, lse, ws),
+                          lambda: kv_attn(q, cache, block_table, kv_lens, cu_q, max_q_len, max_kv_len=max_kv_len, window=window,
+                                          sinks=sinks, scale=scale, out=out, lse=lse, ws=ws))
+    return _kv_attn("kv_attn", q, cache, block_table, kv_lens, cu_q, None, max_q_len, max_kv_len, window, sinks, scale, out,
+                    lse, ws)
+
+
+def kv_attn_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor,
+                 tree: torch.Tensor, max_q_len: int, *, max_kv_len: int = 0, scale: float | None = None,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """kv_attn for a tree of drafted tokens: a sequence's queries are its last
+    positions (already written), each sees every position before them, and of
+    the drafted ones exactly its bits of tree int64 [T][words] (bit e % 64 of word
+    e // 64: drafted token e; a token's own bit among them)."""
+    if stream is not None:
+        return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, tree, out,
+                                   lse, ws),
+                          lambda: kv_attn_tree(q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len=max_kv_len,
+                                               scale=scale, out=out, lse=lse, ws=ws))
+    return _kv_attn("kv_attn_tree", q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, 0, 0, scale, out, lse, ws)
+
+
+def kv_attn_workspace_bytes(q_shape, cache: KVCache, batch: int, max_pages: int, max_q_len: int = 1, max_kv_len: int = 0,
+                            window: int = 0, sinks: int = 0, tree_words: int = 0) -> int:
+    """Bytes of the workspace that kv_attn (kv_attn_tree with tree_words > 0) needs for queries of q_shape."""
+    return int(lib().kv_attn_workspace_bytes(_KV_ATTN.pack(
+        cache.address, 0, 0, 0, 0, max_pages, 0, 256, 0, 0, 0, q_shape[0], batch, max_q_len, max_kv_len, window, sinks,
+        q_shape[1], BF16, tree_words, 1.0)))

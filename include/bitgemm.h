@@ -47,7 +47,8 @@ typedef enum bg_status {
 } bg_status;
 
 typedef enum bg_dtype {
-    BG_F32 = 0, BG_F16 = 1, BG_BF16 = 2, BG_I8 = 3, BG_FP8_E4M3 = 4, BG_I32 = 5
+    BG_F32 = 0, BG_F16 = 1, BG_BF16 = 2, BG_I8 = 3, BG_FP8_E4M3 = 4, BG_I32 = 5,
+    BG_U4 = 6              /* KV cache format only: unsigned 4-bit codes with a zero-point */
 } bg_dtype;
 
 /* Scale granularity ([LPI] §4 "Scale granularity is the key"). */
@@ -470,6 +471,132 @@ int64_t gemm_w4a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 /* The kernel BG_ALGO_AUTO selects for a call of this shape (a BG_ALGO_* value). */
 int gemm_w4a16_algo(int64_t M, int64_t N, int64_t K, int x_dtype);
 int gemm_w8a8_algo(int64_t M, int64_t N, int64_t K, int in_dtype);
+
+/*
+ * The quantized key/value cache ([LPI] §18, §19: keys and values stored in 8
+ * or 4 bits, dequantized inside the attention kernel).
+ *
+ * Pages of page_size tokens, allocated by the caller:
+ *   k, v      codes [pages][kv_heads][page_size][head_dim] bytes (format
+ *             BG_I8 or BG_FP8_E4M3), or [...][head_dim / 2] bytes (BG_U4,
+ *             element 2i in the low nibble)
+ *   k_scales, v_scales
+ *             [pages][kv_heads][page_size] records of 4 bytes: a binary32
+ *             scale s, or for BG_U4 the FP16 scale (low half) and the FP16
+ *             zero-point z (high half).  Values are s * code and s * (u - z).
+ * Slot n is token n % page_size of page n / page_size.
+ * Requires head_dim 64, 128 or 256, page_size a power of two in 16..1024,
+ * 1 <= kv_heads <= 1024, 16-byte aligned buffers.
+ */
+typedef struct bg_kv_cache {
+    void* k;
+    void* v;
+    void* k_scales;
+    void* v_scales;
+    int64_t pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format;
+} bg_kv_cache;
+
+/*
+ * kv_cache_write -- quantize the keys and values of `tokens` new tokens into
+ * their slots, one scale per token and head, by the rules of act_quant_int8 /
+ * act_quant_fp8 (BG_GRAN_ROW) or, for BG_U4, of w4_pack's asymmetric codes
+ * with the zero-point stored in FP16.  A row that holds an infinity or NaN is
+ * stored as codes 0 with a NaN scale: it reads back as NaN, and the codes of
+ * a written slot are always finite.
+ *   k, v     element (t, h, i) at t * token_stride + h * head_stride + i, of
+ *            x_dtype (F32, F16 or BF16); strides in elements, multiples of 16
+ *            bytes, so the slices of a fused projection's rows need no copy
+ *   slots    [tokens]; a slot outside the cache (such as -1) skips its token.
+ *            Two tokens with the same slot race.
+ * tokens = 0 enqueues nothing.
+ */
+bg_status kv_cache_write(const bg_kv_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                         const void* v, int64_t v_token_stride, int64_t v_head_stride, int x_dtype,
+                         const int64_t* slots, int64_t tokens, void* stream);
+
+/*
+ * kv_cache_read -- the values of `tokens` slots: k and v, out [tokens][kv_heads]
+ * [head_dim] of out_dtype (F32, F16 or BF16), one rounding of the binary32
+ * product.  A slot outside the cache reads as zeros.
+ */
+bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                        int out_dtype, void* stream);
+
+/*
+ * kv_attn -- O = softmax(scale * Q K^T) V over the cache, for a batch of
+ * sequences with any number of queries each (one: a decode step; many: a chunk
+ * of a prompt whose own keys and values are already written).
+ *
+ * Query i of sequence b (queries cu_q[b] .. cu_q[b + 1] - 1) stands at position
+ * kv_lens[b] - q_len + i and sees the positions j <= its own with j > own -
+ * window (window > 0; 0: no window) or j < sinks.  Position j is token
+ * j % page_size of page block_table[b][j / page_size]; a page outside the
+ * cache (such as -1) holds nothing, so pages that slid out of the window can
+ * be given back.  Query head h reads kv head h / (q_heads / kv_heads).  A
+ * query that sees nothing gives zeros (lse: -infinity).
+ *
+ * kv_attn_tree -- the same for a tree of drafted tokens: the queries are the
+ * sequence's last q_len positions, each sees every position before them, and
+ * drafted token e exactly where bit e % 64 of tree[t][e / 64] is set (itself
+ * included); bits from 64 * tree_words on are 0.  window must be 0.
+ *
+ * Scores, softmax statistics and sums are binary32; softmax weights are
+ * rounded to FP16 (relative to the largest of their row) for the matrix cores,
+ * the result once to dtype.  Codes of visible slots must be finite (as
+ * kv_cache_write leaves them); what no query of a sequence sees may hold
+ * anything.
+ *   q          element (t, h, i) at t * q_token_stride + h * q_head_stride + i;
+ *              strides multiples of 8 elements
+ *   cu_q       [batch + 1], or NULL: tokens == batch, one query each.  Entries
+ *              are clamped to 0..tokens; rows of out that no sequence owns are
+ *              left alone.
+ *   max_q      at least every sequence's query count (host value: sizes the grid;
+ *              later queries are left alone)
+ *   max_kv     at least every kv_lens entry, or 0 for the block table's width:
+ *              sizes the split over positions; a smaller value costs only speed
+ *   kv_lens    clamped to 0 .. max_pages * page_size
+ *   out        [tokens][q_heads][head_dim] of dtype (F16 or BF16)
+ *   lse        [tokens][q_heads] binary32: ln of the sum of exp(scale * score),
+ *              or NULL
+ *   workspace  16-byte aligned, kv_attn_workspace_bytes(args) bytes, no
+ *              initialisation; calls that share one must not overlap in time
+ * tokens = 0 or batch = 0 enqueues nothing.
+ */
+typedef struct bg_kv_attn {
+    const bg_kv_cache* cache;
+    const void* q;
+    int64_t q_token_stride;
+    int64_t q_head_stride;
+    const int32_t* block_table;
+    int64_t max_pages;
+    const int32_t* kv_lens;
+    const int32_t* cu_q;
+    const uint64_t* tree;
+    void* out;
+    float* lse;
+    int64_t tokens;
+    int64_t batch;
+    int64_t max_q;
+    int64_t max_kv;
+    int64_t window;
+    int64_t sinks;
+    int32_t q_heads;
+    int32_t dtype;
+    int32_t tree_words;
+    float scale;
+} bg_kv_attn;
+
+bg_status kv_attn(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream);
+bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of kv_attn (tree_words == 0) or kv_attn_tree (tree_words > 0)
+ * for these arguments: 0 if none, or if the arguments are not eligible.  Reads
+ * sizes only: apart from cache and cu_q (NULL or not), pointers may be NULL. */
+int64_t kv_attn_workspace_bytes(const bg_kv_attn* args);
 
 /* Static description of a status code. */
 const char* bg_status_string(int status);
