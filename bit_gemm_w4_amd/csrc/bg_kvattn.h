@@ -1,0 +1,288 @@
+// bg_kvattn.h -- what the attention kernels over the KV cache share: which
+// positions a row sees, and codes on their way to FP16 matrix operands.
+#pragma once
+#include "bg_device.h"
+#include "bg_kv.h"
+
+namespace bg {
+
+// Positions are split into `splits` runs of `tiles` visible tiles; the last
+// run takes whatever is left.
+struct KvSplit {
+    int splits, tiles;
+};
+
+// A sequence: its queries are rows q0 .. q0 + len - 1 of q and stand at
+// positions first .. first + len - 1 = kv - 1.
+struct KvSeq {
+    int64_t q0;
+    int len, kv, first;
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
+    KvSeq q;
+    int64_t q0 = b, q1 = b + 1;
+    if (a.cu_q) {
+        q0 = a.cu_q[b];
+        q1 = a.cu_q[b + 1];
+        q0 = q0 < 0 ? 0 : q0 > a.tokens ? a.tokens : q0;
+        q1 = q1 < q0 ? q0 : q1 > a.tokens ? a.tokens : q1;
+    }
+    const int64_t room = a.max_pages << a.c.page_shift, kv = a.kv_lens[b];
+    q.q0 = q0;
+    q.kv = (int)(kv < 0 ? 0 : kv > room ? room : kv);
+    q.len = (int)(q1 - q0);
+    q.first = q.kv - q.len;
+    return q;
+}
+
+// Whether query i of the sequence sees position j < kv (its page aside).
+__device__ __forceinline__ bool kv_sees(const KvAttnArgs& a, const KvSeq& q, int i, int j) {
+    if (a.tree) {
+        const int e = j - q.first;
+        if (e < 0) return j < q.kv;
+        return j < q.kv && e < 64 * a.tree_words && (a.tree[(q.q0 + i) * a.tree_words + (e >> 6)] >> (e & 63) & 1);
+    }
+    const int at = q.first + i;
+    return j <= at && (a.window == 0 || j > at - (int)a.window || j < (int)a.sinks);
+}
+
+// What queries i0 .. i1 see between them: positions [0, sink) and [low, high),
+// as `tiles` tiles of T positions; tile n is tile(n).
+struct KvRange {
+    int low, high, sink, sink_tiles, low_tile, tiles;
+    int all_high, all_low;     // every one of the queries sees [0, all_high), of these but [sink, all_low)
+
+    // Some query may see j.
+    __device__ __forceinline__ bool live(int j) const { return j < high && (j >= low || j < sink); }
+    // Every query sees all of [base, base + n).
+    __device__ __forceinline__ bool whole(int base, int n) const {
+        return base + n <= all_high && (base >= all_low || base + n <= sink);
+    }
+    __device__ __forceinline__ int tile(int n) const { return n < sink_tiles ? n : n - sink_tiles + low_tile; }
+};
+
+template <int T>
+__device__ __forceinline__ KvRange kv_range(const KvAttnArgs& a, const KvSeq& q, int i0, int i1) {
+    KvRange r;
+    if (a.tree) {
+        r.low = r.all_low = r.sink = 0;
+        r.high = q.kv;
+        r.all_high = q.first;
+    } else {
+        const int at0 = q.first + i0, at1 = q.first + i1;
+        r.high = at1 + 1 > 0 ? at1 + 1 : 0;
+        r.all_high = at0 + 1;
+        const int w = (int)a.window;
+        r.low = w && at0 - w + 1 > 0 ? at0 - w + 1 : 0;
+        r.all_low = w && at1 - w + 1 > 0 ? at1 - w + 1 : 0;
+        r.sink = (int)(a.sinks < r.high ? a.sinks : r.high);
+    }
+    r.sink_tiles = (r.sink + T - 1) / T;
+    r.low_tile = r.low / T;
+    if (r.low_tile <= r.sink_tiles) r.sink_tiles = r.low_tile = 0;     // no gap between the two
+    const int end = (r.high + T - 1) / T;
+    r.tiles = r.sink_tiles + (end > r.low_tile ? end - r.low_tile : 0);
+    return r;
+}
+
+// First row of the 16 tokens from position j (a multiple of 16) in the code and
+// record arrays.  Where the position's page does not exist, row 0 of the
+// cache, and bit s of `there` stays clear.
+__device__ __forceinline__ int64_t kv_run(const KvAttnArgs& a, const int32_t* table, int h, int j, uint32_t& there, int s) {
+    const int p = j >> a.c.page_shift;
+    int page = p < a.max_pages ? table[p] : -1;
+    const bool ok = page >= 0 && page < a.c.pages;
+    there |= (ok ? 1u : 0u) << s;
+    page = ok ? page : 0;
+    return (((int64_t)page * a.c.heads + h) << a.c.page_shift) + (ok ? j & ((1 << a.c.page_shift) - 1) : 0);
+}
+
+// How a 16-lane row group holds a row of codes: a key's D codes over 4 lanes,
+// KC chunks of KB bytes each; a value's over 16 lanes, VB bytes each.  Operands
+// hold UNIT^-1 times the code.
+template <int FMT, int D>
+struct KvLayout {
+    static constexpr int PER = FMT == KV_U4 ? 2 : 1;          // codes per byte
+    static constexpr int ROW = D / PER;
+    static constexpr int KB = ROW / 4 < 16 ? ROW / 4 : 16, KC = ROW / (4 * KB), KW = KC * KB / 4;
+    static constexpr int VB = ROW / 16, VW = VB < 4 ? 1 : VB / 4;
+    static constexpr float UNIT = FMT == KV_FP8 ? 1.0f : 512.0f;
+};
+
+template <int N>
+__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* w) {
+    if constexpr (N == 2) {
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (N == 4) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x; w[1] = x.y;
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ float kv_scale(uint32_t record) {
+    return FMT == KV_U4 ? f16_to_f32(record & 0xFFFFu) : __uint_as_float(record);
+}
+
+// A value record for rows that may not see it: a zero-point that is not finite
+// moves to the scale, which only the rows that see the token take.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_masked_record(uint32_t record) {
+    if constexpr (FMT == KV_U4) return (record & 0x7C000000u) == 0x7C000000u ? 0x7E00u : record;
+    return record;
+}
+
+// Two small unsigned integers in the halves of w, read as FP16 subnormals
+// n 2^-24, to n * mul 2^-24 + add: exact.
+__device__ __forceinline__ half2_t small_pair(uint32_t w, _Float16 mul, half2_t add) {
+    return __builtin_elementwise_fma(__builtin_bit_cast(half2_t, w), half2_t{mul, mul}, add);
+}
+
+__device__ __forceinline__ half8_t join4(half2_t a, half2_t b, half2_t c, half2_t d) {
+    return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The zero-point part of a 4-bit operand: -z 2^-9 in both halves.
+__device__ __forceinline__ half2_t minus_zero(uint32_t record) {
+    const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(record >> 16)) * (_Float16)-0x1p-9f;
+    return half2_t{z, z};
+}
+
+// Eight codes (one or two words) to FP16.  4-bit codes come in the order
+// 0 4 1 5 2 6 3 7, which load_query follows.
+template <int FMT>
+__device__ __forceinline__ half8_t codes8(const uint32_t* w, half2_t z) {
+    if constexpr (FMT == KV_FP8) {
+        return join4(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[0], 1.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[0], 1.0f, true),
+                     __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[1], 1.0f, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[1], 1.0f, true));
+    } else if constexpr (FMT == KV_I8) {
+        const half2_t off{(_Float16)-0.25f, (_Float16)-0.25f};        // -128 2^-9
+        const uint32_t a = w[0] ^ 0x80808080u, b = w[1] ^ 0x80808080u;
+        const _Float16 up = (_Float16)0x1p15f;
+        return join4(small_pair(__builtin_amdgcn_perm(0u, a, 0x0c010c00u), up, off), small_pair(__builtin_amdgcn_perm(0u, a, 0x0c030c02u), up, off),
+                     small_pair(__builtin_amdgcn_perm(0u, b, 0x0c010c00u), up, off), small_pair(__builtin_amdgcn_perm(0u, b, 0x0c030c02u), up, off));
+    } else {
+        const _Float16 u0 = (_Float16)0x1p15f, u1 = (_Float16)0x1p11f;
+        const uint32_t a = w[0], b = w[0] >> 8;
+        return join4(small_pair(a & 0x000F000Fu, u0, z), small_pair(a & 0x00F000F0u, u1, z),
+                     small_pair(b & 0x000F000Fu, u0, z), small_pair(b & 0x00F000F0u, u1, z));
+    }
+}
+
+// A key's fragments, one per 32 head elements.
+template <int FMT, int D>
+__device__ __forceinline__ void key_fragments(const uint32_t* w, uint32_t record, half8_t* f) {
+    const half2_t z = FMT == KV_U4 ? minus_zero(record) : half2_t{(_Float16)0.0f, (_Float16)0.0f};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) f[i] = codes8<FMT>(w + i * (FMT == KV_U4 ? 1 : 2), z);
+}
+
+// -z 2^-9 of the value tokens of k-slots 2 n, 2 n + 1.
+__device__ __forceinline__ void value_zeros(const uint32_t* r, uint32_t* vz) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const uint32_t w = r[2 * n] >> 16 | (r[2 * n + 1] & 0xFFFF0000u);
+        vz[n] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w) * half2_t{(_Float16)-0x1p-9f, (_Float16)-0x1p-9f});
+    }
+}
+
+// Element d of a lane's value codes, 8 tokens, to FP16.
+template <int FMT, int D, int VW>
+__device__ __forceinline__ half8_t value_fragment(const uint32_t (&v)[8][VW], const uint32_t* vz, int d) {
+    half2_t x[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        if constexpr (FMT == KV_FP8) {
+            // both elements of a byte pair come from one permute: the compiler shares it
+            const int w = d / 4, i = d % 4 & 2;
+            const uint32_t sel = (uint32_t)(5 + i) << 24 | (uint32_t)(1 + i) << 16 | (uint32_t)(4 + i) << 8 | (uint32_t)i;
+            const uint32_t y = __builtin_amdgcn_perm(v[2 * n + 1][w], v[2 * n][w], sel);
+            x[n] = d & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.0f, false);
+        } else {
+            const int byte = FMT == KV_U4 ? d / 2 : d, w = byte / 4, i = byte % 4;
+            const uint32_t sel = 0x0c000c00u | (uint32_t)(4 + i) << 16 | (uint32_t)i;
+            if constexpr (FMT == KV_I8) {
+                const uint32_t y = __builtin_amdgcn_perm(v[2 * n + 1][w] ^ 0x80808080u, v[2 * n][w] ^ 0x80808080u, sel);
+                x[n] = small_pair(y, (_Float16)0x1p15f, half2_t{(_Float16)-0.25f, (_Float16)-0.25f});
+            } else {
+                const uint32_t y = __builtin_amdgcn_perm(v[2 * n + 1][w], v[2 * n][w], sel);
+                const half2_t z = __builtin_bit_cast(half2_t, vz[n]);
+                x[n] = d & 1 ? small_pair(y & 0x00F000F0u, (_Float16)0x1p11f, z) : small_pair(y & 0x000F000Fu, (_Float16)0x1p15f, z);
+            }
+        }
+    }
+    return join4(x[0], x[1], x[2], x[3]);
+}
+
+// The row's query fragments for lane group g of GROUPS, scaled by a power of
+// two so that FP16 holds them; returns the factor that takes a product of
+// operands to a base-2 exponent.  Rows that are not there are zeros.
+template <int FMT, int D, int GROUPS>
+__device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int g, bool ok, half8_t* f) {
+    using L = KvLayout<FMT, D>;
+    constexpr int N = D / (8 * GROUPS), CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;    // elements a lane holds in a run
+    uint32_t w[N][4];
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int in = i * 8 % CHUNK, c = i * 8 / CHUNK;
+        const int d = c * GROUPS * CHUNK + g * CHUNK + in;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (ok) x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
+        w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float lo = a.bf16 ? __uint_as_float(w[i][n] << 16) : f16_to_f32(w[i][n] & 0xFFFFu);
+            const float hi = a.bf16 ? __uint_as_float(w[i][n] & 0xFFFF0000u) : f16_to_f32(w[i][n] >> 16);
+            top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf(lo), __builtin_fabsf(hi)));
+        }
+    }
+#pragma unroll
+    for (int o = 64 / GROUPS; o < 64; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
+    int e = (int)(__float_as_uint(top) >> 23) - 127;      // top in [2^e, 2^(e + 1))
+    if (e == 128 || top == 0.0f) e = 13;                   // infinities stay, and zeros
+    e = e < -100 ? -100 : e;
+    const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        _Float16 y[8];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float lo = a.bf16 ? __uint_as_float(w[i][n] << 16) : f16_to_f32(w[i][n] & 0xFFFFu);
+            const float hi = a.bf16 ? __uint_as_float(w[i][n] & 0xFFFF0000u) : f16_to_f32(w[i][n] >> 16);
+            y[2 * n] = (_Float16)(lo * up);
+            y[2 * n + 1] = (_Float16)(hi * up);
+        }
+        f[i] = FMT == KV_U4 ? half8_t{y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]}
+                            : half8_t{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+    }
+    return a.scale * 0x1.715476p0f * L::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+}
+
+template <int N>
+__device__ __forceinline__ void store_out(const KvAttnArgs& a, int64_t at, const float* y) {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+    if constexpr (N == 1) {
+        *p = a.bf16 ? f32_to_bf16(y[0]) : f32_to_f16(y[0]);
+    } else {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            w[i] = a.bf16 ? (uint32_t)f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16
+                          : (uint32_t)f32_to_f16(y[2 * i]) | (uint32_t)f32_to_f16(y[2 * i + 1]) << 16;
+        if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+        else if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else {
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+}
+
+}  // namespace bg

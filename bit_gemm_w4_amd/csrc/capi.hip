@@ -629,6 +629,8 @@ bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool poin
     if (st != BG_OK) return st;
     if (p->dtype != BG_F16 && p->dtype != BG_BF16) return fail_in(fn, BG_ERR_DTYPE, "dtype %lld is not F16/BF16", p->dtype);
     if (p->tokens < 0 || p->tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", p->tokens);
+    if (p->tokens * (p->q_heads > 0 ? p->q_heads : 0) > (int64_t(1) << 28))
+        return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld times q_heads=%lld passes 2^28", p->tokens, p->q_heads);
     if (p->batch < 0 || p->batch > kMaxBatch) return fail_in(fn, BG_ERR_SHAPE, "batch=%lld out of range", p->batch);
     if (p->q_heads < a->c.heads || p->q_heads > 16384 || p->q_heads % a->c.heads)
         return fail_in(fn, BG_ERR_SHAPE, "q_heads=%lld is not a multiple of kv_heads=%lld", p->q_heads, a->c.heads);

@@ -1,116 +1,400 @@
-// k_kvattn.hip -- attention over the paged, quantized KV cache.
+// k_kvattn.hip -- attention over the paged, quantized KV cache for few query
+// rows per kv head (decode steps, small draft trees), and the join of split
+// sequences.
 //
-// One wave per (query token, query head): 64 cache tokens at a time, one per
-// lane for the scores, then D / 64 elements per lane for the weighted sum of
-// the values, with the running maximum and sum of the softmax in binary32.
+// Rows are (query token, query head) pairs of one sequence and kv head: the
+// G = q_heads / kv_heads heads of a token share the cache's keys and values,
+// so a block's rows read them once.
+//
+// Bound by HBM: a cache token is 2 D codes and 8 bytes of records per kv
+// head.  A wave takes 32 tokens at a time straight from memory into registers
+// (no LDS, no barrier in the loop), with the next 32 in flight:
+//   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' codes, B = 16 rows
+//   O^T += V^T P^T  the same instruction, A = 16 head elements of 32 tokens
+// The accumulator of S^T holds, in lane (row r, g), tokens 4 g .. 4 g + 3 of
+// each 16; those of two S^T tiles are exactly the 8 k-slots that lane feeds to
+// the second product if V's k-slots are numbered the same way, so the weights
+// go from one product to the next without leaving the lane.  V's codes are
+// loaded as they lie ([token][D], D / 16 codes per lane and token); a byte
+// permute pairs two tokens' codes of one element, which any conversion to FP16
+// needs anyway, and the elements a lane holds become rows of different MFMAs.
+//
+// Numerics.  Codes are exact in FP16 (INT8 and 4-bit codes less their offset,
+// E4M3 values); queries too, each row scaled by a power of two so BF16's range
+// fits (elements below 2^-38 of their row's largest lose bits).  Scales stay in
+// binary32: the key's on the score, the value's on the weight.  The weight times
+// the value's scale, relative to the largest so far of each, is what is rounded
+// to FP16 for the second product: 2^-12 at most, against 2^-9 for BF16.  The
+// reference maximum of a row moves only when a score passes it by 2^8 (weights
+// reach 256 at most), so in the steady state a tile needs no lane exchange.
 #include "bg_device.h"
 #include "bg_internal.h"
-#include "bg_kv.h"
+#include "bg_kvattn.h"
 
 namespace bg {
 namespace {
 
-template <int FMT>
-__device__ __forceinline__ float kv_value(const uint8_t* codes, uint32_t record, int i) {
-    if constexpr (FMT == KV_U4) {
-        const uint32_t u = codes[i / 2] >> (4 * (i % 2)) & 15u;
-        return ((float)u - f16_to_f32(record >> 16)) * f16_to_f32(record & 0xFFFFu);
-    } else if constexpr (FMT == KV_I8) {
-        return (float)(int8_t)codes[i] * __uint_as_float(record);
-    } else {
-        return __builtin_amdgcn_cvt_f32_fp8((int)codes[i], 0) * __uint_as_float(record);
+constexpr int kWaves = 4;
+
+// One 32-token tile of a wave: codes and records of lane (r = lane % 16,
+// g = lane / 16): keys of tokens r and 16 + r, values of its 8 k-slots.
+template <int FMT, int D>
+struct Tile {
+    using L = KvLayout<FMT, D>;
+    uint32_t k[2][L::KW];
+    uint32_t v[8][L::VW];
+    uint32_t ks[8], vs[8];   // records of its k-slots: tokens 4 g .. 4 g + 3 of each 16
+    uint32_t kz[2];          // 4-bit: the record of the token whose key this lane holds
+    uint32_t there;          // bit s: 16 tokens s lie in a page that exists
+
+    __device__ __forceinline__ void load(const KvAttnArgs& a, const int32_t* table, int h, int tile, int r, int g) {
+        there = 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int64_t run = kv_run(a, table, h, tile * 32 + 16 * s, there, s);
+            const uint8_t* kp = a.c.k + run * L::ROW;
+            const uint8_t* vp = a.c.v + run * L::ROW;
+#pragma unroll
+            for (int c = 0; c < L::KC; ++c)
+                load_bytes<L::KB>(kp + (uint32_t)(r * L::ROW + c * 4 * L::KB + g * L::KB), &k[s][c * (L::KB / 4)]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                load_bytes<L::VB>(vp + (uint32_t)((4 * g + j) * L::ROW + r * L::VB), v[4 * s + j]);
+            load_bytes<16>(reinterpret_cast<const uint8_t*>(a.c.ks + run + 4 * g), ks + 4 * s);
+            load_bytes<16>(reinterpret_cast<const uint8_t*>(a.c.vs + run + 4 * g), vs + 4 * s);
+            if constexpr (FMT == KV_U4) kz[s] = a.c.ks[run + r];
+        }
+    }
+};
+
+// RT row tiles of 16 rows per wave.
+template <int FMT, int D, int RT>
+__global__ void __launch_bounds__(kWaves * 64) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    using L = KvLayout<FMT, D>;
+    constexpr int DT = D / 16, ST = D / 32, PAD = D + 4;
+    __shared__ float o_lds[kWaves][16][PAD];
+    __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = blockIdx.x % a.c.heads, rb = blockIdx.x / a.c.heads, split = blockIdx.y, b = blockIdx.z;
+    const KvSeq q = kv_seq(a, b);
+    const int G = a.q_heads / a.c.heads, rows = q.len * G, r0 = rb * 16 * RT;
+    if (r0 >= rows) return;
+    const int last = (rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1;
+    const KvRange rg = kv_range<32>(a, q, r0 / G, last / G);
+    const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
+    const int32_t* table = a.table + b * a.max_pages;
+
+    if (t0 >= t1 && split > 0) {          // nothing left for this split
+        for (int i = threadIdx.x; i <= last - r0; i += kWaves * 64) {
+            const int row = r0 + i;
+            pl[((int64_t)split * a.tokens + q.q0 + row / G) * a.q_heads + h * G + row % G] = -__builtin_inff();
+        }
+        return;
+    }
+
+    half8_t qf[RT][ST];
+    float rq[RT], m[RT], l[RT];
+    int qi[RT];
+    float4_t o[RT][DT];
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        const int row = r0 + 16 * x + r;
+        const bool ok = row < rows;
+        qi[x] = (ok ? row : rows - 1) / G;
+        const int64_t at = (q.q0 + qi[x]) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs;
+        rq[x] = load_query<FMT, D, 4>(a, at, g, ok, qf[x]);
+        m[x] = -__builtin_inff();
+        l[x] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[x][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    uint32_t e_ref = 0;                   // biased exponent that the weights' value scales are relative to
+    float sv_ref = 0.0f;                  // scales below this fit it
+    float f_ref = 0x1p126f;               // 2^(126 - e_ref)
+
+    auto compute = [&](Tile<FMT, D>& t, int tile) {
+        const int base = tile * 32;
+        const bool whole = rg.whole(base, 32) && t.there == 3u;
+        const int first_token = base + 4 * g;   // k-slot j: token first_token + (j & 3) + 16 (j >> 2)
+        if (!whole) {
+            // what no row sees may hold anything: its weight is 0, and so is its value
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool live = (t.there >> (j >> 2) & 1) && rg.live(first_token + (j & 3) + 16 * (j >> 2));
+                t.vs[j] = live ? kv_masked_record<FMT>(t.vs[j]) : 0u;
+#pragma unroll
+                for (int w = 0; w < L::VW; ++w) t.v[j][w] = live ? t.v[j][w] : 0u;
+            }
+        }
+        float sv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sv[j] = kv_scale<FMT>(t.vs[j]);
+        // value scales: the reference exponent follows the largest
+        {
+            float top = sv[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, sv[j]);
+            if (__any(top >= sv_ref)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+                uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top)) >> 23;
+                e = e > 252u ? 252u : e;
+                if (e > e_ref || sv_ref == 0.0f) {
+                    const float f = e - e_ref > 126u ? 0.0f : __uint_as_float((127u - (e - e_ref)) << 23);
+#pragma unroll
+                    for (int x = 0; x < RT; ++x)
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) o[x][d] *= f;
+                    e_ref = e;
+                    f_ref = __uint_as_float((253u - e) << 23);
+                    sv_ref = __uint_as_float((e + 1u) << 23);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sv[j] *= f_ref;
+        }
+        // scores
+        float4_t s[RT][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            half8_t kf[ST];
+            key_fragments<FMT, D>(t.k[u], FMT == KV_U4 ? t.kz[u] : 0u, kf);
+#pragma unroll
+            for (int x = 0; x < RT; ++x) {
+                s[x][u] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < ST; ++c) s[x][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], qf[x][c], s[x][u], 0, 0, 0);
+            }
+        }
+        half8_t p[RT];
+#pragma unroll
+        for (int x = 0; x < RT; ++x) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = s[x][j >> 2][j & 3] * kv_scale<FMT>(t.ks[j]);
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int at = first_token + (j & 3) + 16 * (j >> 2);
+                    y[j] = (t.there >> (j >> 2) & 1) && kv_sees(a, q, qi[x], at) ? y[j] : -__builtin_inff();
+                }
+            }
+            float top = y[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, y[j]);
+            if (__any(top * rq[x] > m[x] + 8.0f)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+                const float mn = __builtin_fmaxf(m[x], top * rq[x]);
+                const float f = mn == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
+                m[x] = mn;
+                l[x] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[x][d] *= f;
+            }
+            const float mx = m[x] == -__builtin_inff() ? 0.0f : m[x];
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], rq[x], -mx));
+                l[x] += w[j];
+                w[j] *= sv[j];
+            }
+            if (!whole) {
+                // a weight of 0 on a scale that is not finite stays 0
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = y[j] == -__builtin_inff() ? 0.0f : w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[x][j] = (_Float16)w[j];
+        }
+        // O^T += V^T P^T
+        uint32_t vz[4];
+        if constexpr (FMT == KV_U4) value_zeros(t.vs, vz);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const half8_t vf = value_fragment<FMT, D>(t.v, vz, d);
+#pragma unroll
+            for (int x = 0; x < RT; ++x) o[x][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[x], o[x][d], 0, 0, 0);
+        }
+    };
+
+    Tile<FMT, D> ta, tb;
+    int i = t0 + wave;
+    if (i < t1) ta.load(a, table, h, rg.tile(i), r, g);
+    for (; i < t1; i += 2 * kWaves) {
+        if (i + kWaves < t1) tb.load(a, table, h, rg.tile(i + kWaves), r, g);
+        compute(ta, rg.tile(i));
+        if (i + kWaves >= t1) break;
+        if (i + 2 * kWaves < t1) ta.load(a, table, h, rg.tile(i + 2 * kWaves), r, g);
+        compute(tb, rg.tile(i + kWaves));
+    }
+
+    // join the waves, 16 rows at a time
+    const float unit = __uint_as_float((e_ref + 1u) << 23) * L::UNIT;
+#pragma unroll
+    for (int x = 0; x < RT; ++x) {
+        l[x] += __shfl_xor(l[x], 16, 64);
+        l[x] += __shfl_xor(l[x], 32, 64);
+        if (x > 0) __syncthreads();
+        if (g == 0) {
+            m_lds[wave][r] = m[x];
+            l_lds[wave][r] = l[x];
+        }
+        __syncthreads();
+        float top = m_lds[0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, m_lds[w][r]);
+        const float f = m[x] == -__builtin_inff() && l[x] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[x] - (top == -__builtin_inff() ? 0.0f : top)) * unit;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int d = 0; d < DT; d += 4) {
+                float4_t y;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = f == 0.0f ? 0.0f : o[x][d + c][n] * f;
+                *reinterpret_cast<float4_t*>(&o_lds[wave][r][(4 * g + n) * DT + d]) = y;
+            }
+        __syncthreads();
+        const int row = r0 + 16 * x + threadIdx.x / 16, part = threadIdx.x % 16;
+        if (row < rows) {
+            const int rr = threadIdx.x / 16;
+            float best = m_lds[0][rr], sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) best = __builtin_fmaxf(best, m_lds[w][rr]);
+            const float base = best == -__builtin_inff() ? 0.0f : best;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                sum += l_lds[w][rr] == 0.0f ? 0.0f : l_lds[w][rr] * __builtin_amdgcn_exp2f(m_lds[w][rr] - base);
+            float y[DT];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) y[d] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+                for (int d = 0; d < DT; d += 4) {
+                    const float4_t z = *reinterpret_cast<const float4_t*>(&o_lds[w][rr][part * DT + d]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[d + c] += z[c];
+                }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int64_t to = (q.q0 + row / G) * a.q_heads + h * G + row % G;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] * inv;
+            const float ls = sum == 0.0f ? -__builtin_inff() : base + __builtin_log2f(sum);
+            if (sp.splits > 1) {
+                float* to_o = po + ((int64_t)split * a.tokens * a.q_heads + to) * D + part * DT;
+#pragma unroll
+                for (int d = 0; d < DT; d += 4) *reinterpret_cast<float4_t*>(to_o + d) = float4_t{y[d], y[d + 1], y[d + 2], y[d + 3]};
+                if (part == 0) pl[(int64_t)split * a.tokens * a.q_heads + to] = ls;
+            } else {
+                store_out<DT>(a, to * D + part * DT, y);
+                if (part == 0 && a.lse) a.lse[to] = ls * 0x1.62e43p-1f;
+            }
+        }
     }
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(64) k_kv_attn_row(KvAttnArgs a) {
-    __shared__ float qs[D];
-    __shared__ float ps[64];
-    __shared__ int64_t rows[64];
-    const int lane = threadIdx.x, hq = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-    int64_t q0 = b, q1 = b + 1;
-    if (a.cu_q) {
-        q0 = a.cu_q[b];
-        q1 = a.cu_q[b + 1];
-        q0 = q0 < 0 ? 0 : q0 > a.tokens ? a.tokens : q0;
-        q1 = q1 < q0 ? q0 : q1 > a.tokens ? a.tokens : q1;
+// Joins the splits of a row: o = sum_s 2^(ls_s - max) o_s / sum_s 2^(ls_s - max).
+// One wave per row; lane s holds split s's weight (64 at a time).
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, const float* po, const float* pl) {
+    const int lane = threadIdx.x & 63, b = blockIdx.y;
+    const KvSeq q = kv_seq(a, b);
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= (int64_t)q.len * a.q_heads) return;
+    const int64_t to = q.q0 * a.q_heads + row, n = a.tokens * a.q_heads;
+    float top = -__builtin_inff();
+    for (int s = lane; s < splits; s += 64) top = __builtin_fmaxf(top, pl[s * n + to]);
+    top = wave_max<64>(top);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    float y[D / 64] = {}, sum = 0.0f;
+    for (int s0 = 0; s0 < splits; s0 += 64) {
+        const float ls = s0 + lane < splits ? pl[(s0 + lane) * n + to] : -__builtin_inff();
+        const float w = __builtin_amdgcn_exp2f(ls - base);
+        sum += w;
+        const int last = splits - s0 < 64 ? splits - s0 : 64;
+        for (int s = 0; s < last; ++s) {
+            const float ws = __shfl(w, s, 64);
+            if (ws == 0.0f) continue;     // a split without tokens wrote no partial
+            const float* p = po + ((int64_t)(s0 + s) * n + to) * D + lane * (D / 64);
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) y[d] += ws * p[d];
+        }
     }
-    if (i >= q1 - q0) return;
-    const int64_t t = q0 + i;
-    int64_t len = a.kv_lens[b];
-    const int64_t room = a.max_pages << a.c.page_shift;
-    len = len < 0 ? 0 : len > room ? room : len;
-    const int64_t first = len - (q1 - q0), pos = first + i;
-    const int h = hq / (a.q_heads / a.c.heads);
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + t * a.q_ts + hq * a.q_hs;
-    for (int d = lane; d < D; d += 64) qs[d] = a.bf16 ? bf16_to_f32(q[d]) : f16_to_f32(q[d]);
-    __syncthreads();
-    constexpr int W = FMT == KV_U4 ? D / 2 : D;
-    float m = -__builtin_inff(), l = 0.0f, o[D / 64] = {};
-    for (int64_t base = 0; base < len; base += 64) {
-        const int64_t j = base + lane;
-        bool seen = j < len;
-        if (a.tree) {
-            const int64_t e = j - first;
-            if (e >= 0) seen = seen && e < 64 * (int64_t)a.tree_words && (a.tree[t * a.tree_words + (e >> 6)] >> (e & 63) & 1);
-        } else {
-            seen = seen && j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
-        }
-        int64_t row = 0;
-        if (seen) {
-            const int page = a.table[b * a.max_pages + (j >> a.c.page_shift)];
-            seen = page >= 0 && page < a.c.pages;
-            row = (((int64_t)page * a.c.heads + h) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
-        }
-        float s = -__builtin_inff();
-        if (seen) {
-            const uint8_t* k = a.c.k + row * W;
-            const uint32_t rec = a.c.ks[row];
-            float acc = 0.0f;
-            for (int d = 0; d < D; ++d) acc += qs[d] * kv_value<FMT>(k, rec, d);
-            s = acc * a.scale;
-        }
-        float mt = wave_max<64>(s);
-        if (!__any(seen)) continue;
-        const float mn = __builtin_fmaxf(m, mt);
-        const float base_m = mn == -__builtin_inff() ? 0.0f : mn;
-        const float alpha = __builtin_expf(m - base_m);
-        const float p = seen ? __builtin_expf(s - base_m) : 0.0f;
-        l = l * alpha + wave_sum<64>(p);
-        m = mn;
-        ps[lane] = p;
-        rows[lane] = seen ? row : -1;
-        __syncthreads();
-        for (int x = 0; x < D / 64; ++x) o[x] *= alpha;
-        for (int n = 0; n < 64; ++n) {
-            if (rows[n] < 0) continue;
-            const uint32_t rec = a.c.vs[rows[n]];
-            for (int x = 0; x < D / 64; ++x) o[x] += ps[n] * kv_value<FMT>(a.c.v + rows[n] * W, rec, x * 64 + lane);
-        }
-        __syncthreads();
+    sum = wave_sum<64>(sum);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] / sum;
+    store_out<D / 64>(a, to * D + lane * (D / 64), y);
+    if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
+}
+
+template <typename F>
+void for_format(int fmt, int dim, F&& f) {
+    auto on_dim = [&](auto FMT) {
+        if (dim == 64) f(FMT, std::integral_constant<int, 64>{});
+        else if (dim == 128) f(FMT, std::integral_constant<int, 128>{});
+        else f(FMT, std::integral_constant<int, 256>{});
+    };
+    if (fmt == KV_I8) on_dim(std::integral_constant<int, KV_I8>{});
+    else if (fmt == KV_FP8) on_dim(std::integral_constant<int, KV_FP8>{});
+    else on_dim(std::integral_constant<int, KV_U4>{});
+}
+
+// Rows of a block, and how positions are split over blocks.
+struct Plan {
+    int rt;
+    unsigned row_blocks;
+    KvSplit sp;
+};
+
+Plan plan_of(const KvAttnArgs& a) {
+    Plan p;
+    const int64_t rows = a.max_q * (a.q_heads / a.c.heads);
+    p.rt = rows <= 16 || a.c.dim == 256 ? 1 : 2;
+    p.row_blocks = (unsigned)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    // positions a row block can see, in 32-token tiles
+    int64_t seen = a.max_kv;
+    if (a.window) {
+        const int64_t most = a.window + a.max_q + 64 + (a.sinks ? a.sinks + 64 : 0);
+        seen = most < seen ? most : seen;
     }
-    for (int x = 0; x < D / 64; ++x) {
-        const float y = l == 0.0f ? 0.0f : o[x] / l;
-        static_cast<uint16_t*>(a.out)[(t * a.q_heads + hq) * D + x * 64 + lane] = a.bf16 ? f32_to_bf16(y) : f32_to_f16(y);
-    }
-    if (a.lse && lane == 0) a.lse[t * a.q_heads + hq] = l == 0.0f ? -__builtin_inff() : m + __builtin_logf(l);
+    const int64_t tiles = (seen + 31) / 32 > 0 ? (seen + 31) / 32 : 1;
+    const int64_t blocks = a.batch * a.c.heads * p.row_blocks;
+    int64_t splits = (1024 + blocks - 1) / blocks;
+    const int64_t most = (tiles + 7) / 8;
+    splits = splits > most ? most : splits;
+    splits = splits > 256 ? 256 : splits < 1 ? 1 : splits;
+    p.sp.tiles = (int)((tiles + splits - 1) / splits);
+    p.sp.splits = (int)((tiles + p.sp.tiles - 1) / p.sp.tiles);
+    return p;
 }
 
 }  // namespace
 
-int64_t kv_attn_workspace(const KvAttnArgs&) { return 0; }
+int64_t kv_attn_workspace(const KvAttnArgs& a) {
+    const Plan p = plan_of(a);
+    return p.sp.splits > 1 ? (int64_t)p.sp.splits * a.tokens * a.q_heads * (a.c.dim + 1) * 4 : 0;
+}
 
-const char* launch_kv_attn(const KvAttnArgs& a, void*, hipStream_t s) {
-    const dim3 grid((unsigned)a.q_heads, (unsigned)a.max_q, (unsigned)a.batch);
-    auto on_dim = [&](auto FMT) {
-        if (a.c.dim == 64) k_kv_attn_row<FMT(), 64><<<grid, 64, 0, s>>>(a);
-        else if (a.c.dim == 128) k_kv_attn_row<FMT(), 128><<<grid, 64, 0, s>>>(a);
-        else k_kv_attn_row<FMT(), 256><<<grid, 64, 0, s>>>(a);
-    };
-    if (a.c.fmt == KV_I8) on_dim(std::integral_constant<int, KV_I8>{});
-    else if (a.c.fmt == KV_FP8) on_dim(std::integral_constant<int, KV_FP8>{});
-    else on_dim(std::integral_constant<int, KV_U4>{});
-    return kname("k_kv_attn_row", a.c.fmt, a.c.dim);
+const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
+    const Plan p = plan_of(a);
+    float* po = static_cast<float*>(ws);
+    float* pl = po + (int64_t)p.sp.splits * a.tokens * a.q_heads * a.c.dim;
+    const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, (unsigned)a.batch);
+    for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
+        if (p.rt == 1) k_kv_attn_few<FMT(), D(), 1><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
+        else if constexpr (D() != 256) k_kv_attn_few<FMT(), D(), 2><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
+    });
+    if (p.sp.splits > 1) {
+        const dim3 join((unsigned)((a.max_q * a.q_heads + 3) / 4), (unsigned)a.batch);
+        if (a.c.dim == 64) k_kv_attn_join<64><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+        else if (a.c.dim == 128) k_kv_attn_join<128><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+        else k_kv_attn_join<256><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+    }
+    return kname("k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
 }
 
 }  // namespace bg
