@@ -1,6 +1,8 @@
 // bg_kvattn.h -- what the attention kernels over the KV cache share: which
 // positions a row sees, and codes on their way to FP16 matrix operands.
 #pragma once
+#include <type_traits>
+
 #include "bg_device.h"
 #include "bg_kv.h"
 
@@ -54,10 +56,10 @@ struct KvRange {
     int all_high, all_low;     // every one of the queries sees [0, all_high), of these but [sink, all_low)
 
     // Some query may see j.
-    __device__ __forceinline__ bool live(int j) const { return j < high && (j >= low || j < sink); }
+    __device__ __forceinline__ bool live(int j) const { return (j < high) & ((j >= low) | (j < sink)); }
     // Every query sees all of [base, base + n).
     __device__ __forceinline__ bool whole(int base, int n) const {
-        return base + n <= all_high && (base >= all_low || base + n <= sink);
+        return (base + n <= all_high) & ((base >= all_low) | (base + n <= sink));
     }
     __device__ __forceinline__ int tile(int n) const { return n < sink_tiles ? n : n - sink_tiles + low_tile; }
 };
@@ -265,6 +267,63 @@ __device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int
     return a.scale * 0x1.715476p0f * L::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 }
 
+// The same for a block of WAVES waves of 32 rows, two lane groups, in fragments of 8
+// elements c = 0 .. D / 16 - 1 that follow the keys' order (fragment 4 i + n of a
+// key is the i-th of lane group n), scaled by one power of two: the largest finite element of
+// all its rows lands in [2^13, 2^14).
+template <int FMT, int D, int WAVES>
+__device__ __forceinline__ float load_block_queries(const KvAttnArgs& a, int64_t at, int g, bool ok, int wave, float* lds, half8_t* f) {
+    using L = KvLayout<FMT, D>;
+    constexpr int N = D / 16, CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;
+    float top = 0.0f;
+    auto pair = [&](uint32_t w, float& lo, float& hi) {
+        lo = a.bf16 ? __uint_as_float(w << 16) : f16_to_f32(w & 0xFFFFu);
+        hi = a.bf16 ? __uint_as_float(w & 0xFFFF0000u) : f16_to_f32(w >> 16);
+    };
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int i = c >> 1, n = 2 * (c & 1) + g;
+        const int d = i * 8 / CHUNK * 4 * CHUNK + n * CHUNK + i * 8 % CHUNK;
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (ok) y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            pair(w[k], lo, hi);
+            lo = __builtin_fabsf(lo);
+            hi = __builtin_fabsf(hi);
+            top = __builtin_fmaxf(top, lo < __builtin_inff() ? lo : 0.0f);
+            top = __builtin_fmaxf(top, hi < __builtin_inff() ? hi : 0.0f);
+        }
+        f[c] = __builtin_bit_cast(half8_t, y);
+    }
+    top = wave_max<64>(top);
+    if ((threadIdx.x & 63) == 0) lds[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = __builtin_fmaxf(top, lds[w]);
+    int e = top == 0.0f ? 13 : (int)(__float_as_uint(top) >> 23) - 127;
+    e = __builtin_amdgcn_readfirstlane(e < -100 ? -100 : e);
+    const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const uint4 v = __builtin_bit_cast(uint4, f[c]);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        _Float16 y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            pair(w[k], lo, hi);
+            y[2 * k] = (_Float16)(lo * up);
+            y[2 * k + 1] = (_Float16)(hi * up);
+        }
+        f[c] = FMT == KV_U4 ? half8_t{y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]}
+                            : half8_t{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+    }
+    return a.scale * 0x1.715476p0f * L::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+}
+
 template <int N>
 __device__ __forceinline__ void store_out(const KvAttnArgs& a, int64_t at, const float* y) {
     uint16_t* p = static_cast<uint16_t*>(a.out) + at;
@@ -284,5 +343,21 @@ __device__ __forceinline__ void store_out(const KvAttnArgs& a, int64_t at, const
         }
     }
 }
+
+// f(FMT, D) over the formats and head sizes.
+template <typename F>
+void for_format(int fmt, int dim, F&& f) {
+    auto on_dim = [&](auto FMT) {
+        if (dim == 64) f(FMT, std::integral_constant<int, 64>{});
+        else if (dim == 128) f(FMT, std::integral_constant<int, 128>{});
+        else f(FMT, std::integral_constant<int, 256>{});
+    };
+    if (fmt == KV_I8) on_dim(std::integral_constant<int, KV_I8>{});
+    else if (fmt == KV_FP8) on_dim(std::integral_constant<int, KV_FP8>{});
+    else on_dim(std::integral_constant<int, KV_U4>{});
+}
+
+// Many query rows per kv head, rows of row_blocks blocks (k_kvattn_many.hip).
+const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, float* po, float* pl, hipStream_t s);
 
 }  // namespace bg

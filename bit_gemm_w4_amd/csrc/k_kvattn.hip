@@ -331,20 +331,9 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
     if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
 }
 
-template <typename F>
-void for_format(int fmt, int dim, F&& f) {
-    auto on_dim = [&](auto FMT) {
-        if (dim == 64) f(FMT, std::integral_constant<int, 64>{});
-        else if (dim == 128) f(FMT, std::integral_constant<int, 128>{});
-        else f(FMT, std::integral_constant<int, 256>{});
-    };
-    if (fmt == KV_I8) on_dim(std::integral_constant<int, KV_I8>{});
-    else if (fmt == KV_FP8) on_dim(std::integral_constant<int, KV_FP8>{});
-    else on_dim(std::integral_constant<int, KV_U4>{});
-}
-
 // Rows of a block, and how positions are split over blocks.
 struct Plan {
+    bool many;
     int rt;
     unsigned row_blocks;
     KvSplit sp;
@@ -353,17 +342,23 @@ struct Plan {
 Plan plan_of(const KvAttnArgs& a) {
     Plan p;
     const int64_t rows = a.max_q * (a.q_heads / a.c.heads);
+    // Up to 96 rows the few-row kernel is ahead (64 rows of 16 x 8192 tokens, E4M3: 116
+    // against 131 us; 128 rows: 173 against 138).
+    p.many = rows > 96;
     p.rt = rows <= 16 || a.c.dim == 256 ? 1 : 2;
-    p.row_blocks = (unsigned)((rows + 16 * p.rt - 1) / (16 * p.rt));
-    // positions a row block can see, in 32-token tiles
+    const int per_block = p.many ? (a.c.dim == 256 ? 128 : 256) : 16 * p.rt, tile = p.many ? 64 : 32;
+    p.row_blocks = (unsigned)((rows + per_block - 1) / per_block);
+    // positions a row block can see, in tiles
     int64_t seen = a.max_kv;
     if (a.window) {
         const int64_t most = a.window + a.max_q + 64 + (a.sinks ? a.sinks + 64 : 0);
         seen = most < seen ? most : seen;
     }
-    const int64_t tiles = (seen + 31) / 32 > 0 ? (seen + 31) / 32 : 1;
+    const int64_t tiles = (seen + tile - 1) / tile > 0 ? (seen + tile - 1) / tile : 1;
     const int64_t blocks = a.batch * a.c.heads * p.row_blocks;
-    int64_t splits = (1024 + blocks - 1) / blocks;
+    // Many rows: one block a CU and one round of them, a block's start being worth four
+    // tiles (64-row trees over 16 x 8192 tokens: 193 us with 256 blocks, 204 with 512).
+    int64_t splits = ((p.many ? 256 : 1024) + blocks - 1) / blocks;
     const int64_t most = (tiles + 7) / 8;
     splits = splits > most ? most : splits;
     splits = splits > 256 ? 256 : splits < 1 ? 1 : splits;
@@ -384,7 +379,9 @@ const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
     float* po = static_cast<float*>(ws);
     float* pl = po + (int64_t)p.sp.splits * a.tokens * a.q_heads * a.c.dim;
     const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, (unsigned)a.batch);
-    for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
+    const char* name = nullptr;
+    if (p.many) name = launch_kv_attn_many(a, p.sp, p.row_blocks, po, pl, s);
+    else for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
         if (p.rt == 1) k_kv_attn_few<FMT(), D(), 1><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
         else if constexpr (D() != 256) k_kv_attn_few<FMT(), D(), 2><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
     });
@@ -394,7 +391,7 @@ const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
         else if (a.c.dim == 128) k_kv_attn_join<128><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
         else k_kv_attn_join<256><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
     }
-    return kname("k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
+    return name ? name : kname("k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
 }
 
 }  // namespace bg

@@ -1,0 +1,497 @@
+// k_kvattn_many.hip -- attention over the paged, quantized KV cache for many
+// query rows per kv head (prompt chunks, large draft trees).
+//
+// A block of eight waves takes 256 rows of one sequence and kv head, 32 to a wave
+// (head size 256: four waves, 128 rows), and walks the positions some row sees
+// in tiles of 64.  With this many rows per cache byte the matrix cores bound it:
+//   S^T = K Q^T     v_mfma_f32_32x32x16_f16, A = 32 tokens, B = 32 rows
+//   O^T += V^T P^T  A = 32 head elements of 16 tokens, B = the weights in place
+// (the k-slots of V are numbered as the accumulator of S^T holds its tokens).
+// 32x32x16 and not 16x16x32: beside the latter's 16-cycle products the vector
+// units issue little (16 products with 4 multiply-adds and an exponential
+// between each: 478 ns of two waves, against 433 ns for the products alone; the
+// same work in 16x16x32: 844 ns).
+//
+// What else there is to do runs beside the products:
+// * A tile's codes turn to FP16 once per block, in LDS, as the fragments that the
+//   waves' products take (16 bytes per lane, contiguous over lanes: no bank
+//   conflicts in either direction).  Four waves carry keys, two tiles ahead, four
+//   values, one ahead; one barrier a tile.  The two waves of a SIMD carry at
+//   different times: the values' after the first of a tile's two steps.
+// * The products of the next step's scores and of the last step's values alternate
+//   (two chains that do not wait for one another), with this step's weights in the
+//   vector units' slots between them.
+// A tile of 64 positions takes a block about 2.0 us (4,300 cycles, 2,048 of them in
+// each SIMD's matrix core); a block's start (pages, first codes, queries) 8 us, so
+// blocks are made as few as fill the device once.  2,048 queries over a window
+// of 4,096 in E4M3 (8 kv heads of 4, D = 128): 185 us, 742 TFLOP/s; the few-row
+// kernel takes 460 us.
+//
+// Numerics as in the few-row kernel: codes exact in FP16, scales and statistics
+// in binary32.  Two things differ, both to spare vector instructions.  Queries are
+// scaled by one power of two per block, not per row, so the score's factors fold
+// into the token's scale (a query element below 2^-30 of the largest of the
+// block's rows loses BF16 bits; its score then errs by 2^-38 of the largest |q| |k|
+// there at most).  The weights are taken against the running reference before
+// their maximum is known, and only if a lane's sum passes 2^8 is the maximum
+// found, the reference moved and the weights taken again.
+#include "bg_device.h"
+#include "bg_internal.h"
+#include "bg_kvattn.h"
+
+namespace bg {
+namespace {
+
+constexpr int kT = 64, kRows = 32;          // positions of a tile, rows of a wave
+
+// Sixteen lanes' or 32 lanes' worth of a value row: VB bytes and E elements a lane.
+template <int FMT, int D>
+struct ManyLayout {
+    using L = KvLayout<FMT, D>;
+    static constexpr int LR = L::ROW >= 64 ? 32 : 16;
+    static constexpr int VB = L::ROW / LR, VW = VB < 4 ? 1 : VB / 4, E = VB * L::PER;
+};
+
+template <int FMT, int D>
+struct ManyLds {
+    static constexpr int KRING = D == 256 ? 4 : 5, VRING = 5;
+    half8_t k[KRING][D / 8][32];      // [step mod KRING][8 elements][token]
+    half8_t v[VRING][2][2][D];        // [step mod VRING][16 tokens][lane half][element e of lane r at e LR + r]
+    float ks[4][kT], vs[4][kT];       // [tile mod 4]: key scales times the queries' unit, value scales over 2^(e - 126)
+    uint32_t e[4];                    // [tile mod 4]
+    float top[8];
+};
+
+// Where a sequence's tokens of one head lie.
+struct ManyPages {
+    const int32_t* table;
+    int last, shift;           // last entry of the table
+    uint32_t pages, rows, row; // pages of the cache, rows of a page, first row of the head in it
+
+    __device__ __forceinline__ ManyPages(const KvAttnArgs& a, int b, int h)
+        : table(a.table + b * a.max_pages), last((int)a.max_pages - 1), shift(a.c.page_shift), pages((uint32_t)a.c.pages),
+          rows((uint32_t)a.c.heads << a.c.page_shift), row((uint32_t)h << a.c.page_shift) {}
+    // Positions past the table are past every sequence: what is read for them is masked.
+    __device__ __forceinline__ uint32_t page(int position) const {
+        const int p = position >> shift;
+        return (uint32_t)table[p < last ? p : last];
+    }
+    __device__ __forceinline__ bool there(uint32_t page) const { return page < pages; }
+    // Offset in an array of `unit` bytes per token and head (in page 0 if the page does not exist); a page's bytes fit 32 bits.
+    __device__ __forceinline__ uint64_t at(uint32_t page, int position, uint32_t unit) const {
+        return (uint64_t)(there(page) ? page : 0u) * (rows * unit) + (row + (uint32_t)(position & ((1 << shift) - 1))) * unit;
+    }
+};
+
+// Sixteen tokens' keys or values on their way from memory to LDS.
+template <int FMT, int D>
+struct ManyStage {
+    using L = KvLayout<FMT, D>;
+    using M = ManyLayout<FMT, D>;
+    static constexpr int W = L::KW > 8 * M::VW ? L::KW : 8 * M::VW;
+    uint32_t c[W], z[FMT == KV_U4 ? 8 : 1];
+
+    // The 16 tokens from position `first`, of page `page`.
+    __device__ __forceinline__ void load_keys(const KvAttnArgs& a, const ManyPages& p, uint32_t page, int first, int lane) {
+        const uint8_t* kp = a.c.k + (p.at(page, first, L::ROW) + (uint32_t)((lane & 15) * L::ROW + (lane >> 4) * L::KB));
+#pragma unroll
+        for (int i = 0; i < L::KC; ++i) load_bytes<L::KB>(kp + i * 4 * L::KB, &c[i * (L::KB / 4)]);
+        if constexpr (FMT == KV_U4) load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + (p.at(page, first, 4) + 4 * (lane & 15)), z);
+    }
+    __device__ __forceinline__ void store_keys(half8_t (&t)[D / 8][32], int s, int lane) {
+        half8_t f[D / 32];
+        key_fragments<FMT, D>(c, z[0], f);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) t[4 * i + (lane >> 4)][16 * s + (lane & 15)] = f[i];
+    }
+
+    // A lane's 8 k-slots: tokens 4 half .. + 3 and 8 + 4 half .. + 3.
+    __device__ __forceinline__ void load_values(const KvAttnArgs& a, const ManyPages& p, uint32_t page, int first, int lane) {
+        const int half = lane >> 5, r = lane & (M::LR - 1);
+        const uint8_t* vp = a.c.v + (p.at(page, first, L::ROW) + (uint32_t)(4 * half * L::ROW + r * M::VB));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) load_bytes<M::VB>(vp + ((j & 3) + 8 * (j >> 2)) * L::ROW, &c[j * M::VW]);
+        if constexpr (FMT == KV_U4) {
+            const uint8_t* zp = reinterpret_cast<const uint8_t*>(a.c.vs) + (p.at(page, first, 4) + 16 * half);
+            load_bytes<16>(zp, z);
+            load_bytes<16>(zp + 32, z + 4);
+        }
+    }
+    __device__ __forceinline__ void store_values(half8_t (&t)[2][D], const KvRange& rg, int first, bool there, bool whole, int lane) {
+        const int half = lane >> 5, r = lane & 31;
+        uint32_t v[8][M::VW];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int n = 0; n < M::VW; ++n) v[j][n] = c[j * M::VW + n];
+        if (!whole) {
+            // what no row sees may hold anything: its value becomes 0
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool live = there & rg.live(first + 4 * half + (j & 3) + 8 * (j >> 2));
+#pragma unroll
+                for (int n = 0; n < M::VW; ++n) v[j][n] = live ? v[j][n] : 0u;
+                if constexpr (FMT == KV_U4) z[j] = live ? z[j] : 0u;
+            }
+        }
+        if (r < M::LR) {
+            uint32_t y[4];
+            if constexpr (FMT == KV_U4) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = kv_masked_record<FMT>(z[j]);
+                value_zeros(z, y);
+            }
+#pragma unroll
+            for (int e = 0; e < M::E; ++e) t[half][e * M::LR + r] = value_fragment<FMT, D>(v, y, e);
+        }
+    }
+};
+
+// Bit j: the row sees position base + j.
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+__device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& q, int i, int base, uint64_t there) {
+    uint64_t m;
+    if (a.tree) {
+        m = low_bits(q.first - base);
+        const int e = base - q.first;            // bit 0's drafted token
+        const uint64_t* w = a.tree + (q.q0 + i) * a.tree_words;
+        const int n = e >> 6, sh = e & 63;
+        uint64_t bits = n >= 0 && n < a.tree_words ? w[n] >> sh : 0;
+        if (sh && n + 1 >= 0 && n + 1 < a.tree_words) bits |= w[n + 1] << (64 - sh);
+        m |= bits & ~low_bits(-e);
+        m &= low_bits(q.kv - base);
+    } else {
+        const int at = q.first + i;
+        m = low_bits(at + 1 - base);
+        if (a.window) m &= ~low_bits(at - (int)a.window + 1 - base) | low_bits((int)a.sinks - base);
+    }
+    return m & there;
+}
+
+template <int FMT, int D, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    using L = KvLayout<FMT, D>;
+    using M = ManyLayout<FMT, D>;
+    constexpr int DT = D / 32, ST = D / 16, RUNS = 8 / WAVES;
+    __shared__ ManyLds<FMT, D> lds;
+
+    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = blockIdx.x % a.c.heads, split = blockIdx.y, b = blockIdx.z;
+    const int rb = gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads;     // the longest first
+    const KvSeq q = kv_seq(a, b);
+    const int G = a.q_heads / a.c.heads, rows = q.len * G, r0 = rb * WAVES * kRows;
+    if (r0 >= rows) return;
+    const int last = (rows < r0 + WAVES * kRows ? rows : r0 + WAVES * kRows) - 1;
+    const KvRange rg = kv_range<kT>(a, q, r0 / G, last / G);
+    const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
+    const int nt = t1 - t0;               // tiles of this block: number i is tile t0 + i of the range
+    if (nt <= 0 && split > 0) {          // nothing left for this split
+        for (int i = threadIdx.x; i <= last - r0; i += WAVES * 64) {
+            const int row = r0 + i;
+            pl[((int64_t)split * a.tokens + q.q0 + row / G) * a.q_heads + h * G + row % G] = -__builtin_inff();
+        }
+        return;
+    }
+
+    const int w0 = r0 + wave * kRows;     // the wave's first row
+    const bool has_rows = w0 < rows;
+    const int wlast = rows < w0 + kRows ? rows - 1 : w0 + kRows - 1;
+    const KvRange wr = kv_range<kT>(a, q, (has_rows ? w0 : rows - 1) / G, wlast / G);
+    const int row = w0 + r;
+    const bool ok = row < rows;
+    const int qi = (ok ? row : rows - 1) / G;
+    const int64_t to = (q.q0 + qi) * a.q_heads + h * G + (ok ? row % G : 0);
+
+    half8_t qf[ST];
+    float unit_s = 0.0f;
+    float16_t o[DT], s[2];
+    float nm = __builtin_inff(), l = 0.0f;             // minus the reference, the sum
+    uint32_t e_ref = 0, e_next = 0;                    // O is over 2^(e_ref - 126), the next tile's values over e_next's
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = float16_t{} ;
+
+    // Step n is tokens 32 (n % 2) of the block's tile n / 2.  At step n the matrix cores take the
+    // scores of step n + 1 and the values of step n - 1 in turn, and the vector units the
+    // weights of step n.  A fragment's register (keys: elements 16 c of 32 tokens;
+    // values: elements 32 d of 16 tokens t at t DT + d) takes the one FK (FV) further on
+    // as soon as its product is issued.
+    constexpr int FK = D == 256 ? ST : 4, FV = 4;
+    half8_t fk[FK], fv[FV], p[2][2];
+    float4_t kr, vr;                                   // scales of the 4 tokens that come next
+    auto key = [&](int n, int c) { return lds.k[(uint32_t)(n + 5) % lds.KRING][2 * c + g][r]; };
+    auto value = [&](int n, int j) { return lds.v[(uint32_t)(n + 5) % lds.VRING][j / DT][g][32 * (j % DT) + r]; };
+    auto k_scale = [&](int n, int x) { return *reinterpret_cast<const float4_t*>(&lds.ks[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]); };
+    auto v_scale = [&](int n, int x) { return *reinterpret_cast<const float4_t*>(&lds.vs[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]); };
+    // The scores of an even step n, with the fragments that follow; step n - 1 weighs nothing.
+    auto start = [&](int n) {
+        half8_t f[ST];
+#pragma unroll
+        for (int c = 0; c < ST; ++c) f[c] = key(n, c);
+        s[0] = float16_t{};
+#pragma unroll
+        for (int c = 0; c < ST; ++c) s[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[c], qf[c], s[0], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < FK; ++c) fk[c] = key(n + 1, c);
+#pragma unroll
+        for (int j = 0; j < FV; ++j) fv[j] = half8_t{};
+        p[1][0] = p[1][1] = half8_t{};
+        kr = k_scale(n, 0);
+        vr = v_scale(n, 0);
+    };
+    // The values of an odd step, of which FV fragments are here.
+    auto finish = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+            o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(j < FV ? fv[j % FV] : value(n, j), p[1][j / DT], o[j % DT], 0, 0, 0);
+        p[1][0] = p[1][1] = half8_t{};
+    };
+    auto attend = [&](int i, auto U, bool whole, uint64_t seen) {
+        constexpr int u = U();
+        const int n = 2 * i + u;
+        float sum = 0.0f;
+        s[1 - u] = float16_t{};
+        auto products = [&](int c) {
+            s[1 - u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fk[c % FK], qf[c], s[1 - u], 0, 0, 0);
+            fk[c % FK] = c + FK < ST ? key(n + 1, c + FK) : key(n + 2, c + FK - ST);
+            o[c % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fv[c % FV], p[1 - u][c / DT], o[c % DT], 0, 0, 0);
+            fv[c % FV] = c + FV < ST ? value(n - 1, c + FV) : value(n, c + FV - ST);
+        };
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float4_t kn = kr, vn = vr;
+            if (x < 3) {
+                kr = k_scale(n, x + 1);
+                vr = v_scale(n, x + 1);
+            }
+#pragma unroll
+            for (int c = x * ST / 4; c < (x + 1) * ST / 4; ++c) products(c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], nm));
+                sum += w;
+                p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(w * vn[j]);
+            }
+            if (x < 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        const bool again = (uint32_t)!whole | (uint32_t)(__ballot(!(sum <= 256.0f)) != 0) | (uint32_t)(u == 1 && e_next != e_ref);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(p[u][j]));
+        kr = k_scale(n + 1, 0);
+        vr = v_scale(n + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (again) {
+            const uint32_t see = (uint32_t)(seen >> (32 * u + 4 * g));     // bit 8 (j / 4) + j % 4: the row sees k-slot j
+            auto in = [&](int x, int j) { return see >> (8 * x + j) & 1; };
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4_t kn = k_scale(n, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = in(x, j) ? __builtin_fmaxf(top, s[u][4 * x + j] * kn[j]) : top;
+            }
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+            const float ref = top + nm > 4.0f || nm == __builtin_inff() ? __builtin_fminf(nm, -top) : nm;      // the reference only rises
+            float x = nm == __builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ref - nm), v = 1.0f;
+            nm = ref;
+            l *= x;
+            if (u == 1) {
+                // from here on values are over the next tile's scale
+                v = e_next - e_ref > 126u ? 0.0f : __uint_as_float((127u - (e_next - e_ref)) << 23);
+                x *= v;
+                e_ref = e_next;
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= x;
+            sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4_t kn = k_scale(n, x), vn = v_scale(n, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // what the row does not see weighs 0, whatever its scales hold
+                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], nm)) : 0.0f;
+                    sum += w;
+                    p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * vn[j] * v : 0.0f);
+                }
+            }
+        }
+        l += sum;
+    };
+
+    // Half of the waves carry keys (and the first of them the scales), two tiles ahead,
+    // the others values, one ahead.
+    struct Carry {
+        ManyStage<FMT, D> st[RUNS];
+        uint32_t k, v;                                 // records
+    };
+    struct Pages {
+        uint32_t own[RUNS], lane;                      // of the wave's tokens, of token `lane`
+    };
+    const ManyPages pages(a, b, h);
+    const bool keys = wave < WAVES / 2;
+    const int role = keys ? wave : wave - WAVES / 2;
+    float sv_ref = 0.0f, f_ref = 0x1p126f;             // value scales below sv_ref fit the reference 2^(e_put - 126) = 1 / f_ref
+    uint32_t e_put = 0;
+    // Past the last tile the last one is staged again, into parts that nothing reads.
+    auto base_of = [&](int i) { return rg.tile(t0 + (i < nt ? i : nt - 1)) * kT; };
+    auto find = [&](Pages& p, int i) {
+        const int base = base_of(i);
+#pragma unroll
+        for (int n = 0; n < RUNS; ++n) p.own[n] = pages.page(base + 16 * (role * RUNS + n));
+        p.lane = pages.page(base + lane);
+    };
+    // Asks for tile i's part of this wave; bit n of the result: token n lies in a page that exists.
+    auto load = [&](Carry& c, const Pages& p, int i) -> uint64_t {
+        const int base = base_of(i);
+        if (keys) {
+#pragma unroll
+            for (int n = 0; n < RUNS; ++n) c.st[n].load_keys(a, pages, p.own[n], base + 16 * (role * RUNS + n), lane);
+            if (role == 0) {
+                const uint64_t at = pages.at(p.lane, base + lane, 4);
+                load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + at, &c.k);
+                load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.vs) + at, &c.v);
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < RUNS; ++n) c.st[n].load_values(a, pages, p.own[n], base + 16 * (role * RUNS + n), lane);
+        }
+        return __ballot(pages.there(p.lane));
+    };
+    auto store = [&](Carry& c, int i, uint64_t there) {
+        const int base = base_of(i);
+        const bool whole = (there == ~0ull) & rg.whole(base, kT);
+        if (!keys) {
+#pragma unroll
+            for (int n = 0; n < RUNS; ++n) {
+                const int run = role * RUNS + n;
+                c.st[n].store_values(lds.v[(uint32_t)(2 * i + (run >> 1) + 5) % lds.VRING][run & 1], rg, base + 16 * run, there >> (16 * run) & 1, whole, lane);
+            }
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < RUNS; ++n) c.st[n].store_keys(lds.k[(uint32_t)(2 * i + ((role * RUNS + n) >> 1) + 5) % lds.KRING], (role * RUNS + n) & 1, lane);
+        if (role == 0) {
+            float sv = kv_scale<FMT>(kv_masked_record<FMT>(c.v));
+            if (!whole) sv = (bool)(there >> lane & 1) & rg.live(base + lane) ? sv : 0.0f;
+            if (__any(sv >= sv_ref)) {
+                uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(sv))) >> 23;
+                e = e > 252u ? 252u : e;
+                if (e > e_put || sv_ref == 0.0f) {
+                    e_put = e;
+                    f_ref = __uint_as_float((253u - e) << 23);
+                    sv_ref = __uint_as_float((e + 1u) << 23);
+                }
+            }
+            lds.ks[i & 3][lane] = kv_scale<FMT>(c.k) * unit_s;
+            lds.vs[i & 3][lane] = sv * f_ref;
+            lds.e[i & 3] = e_put;
+        }
+    };
+
+    // th0 to th2: the tokens that are there of tiles i, i + 1 and i + 2 (th2: keys only)
+    Carry st;
+    Pages pg;                                          // of the tile to load next
+    uint64_t th0 = 0, th1 = 0, th2 = 0;
+    {
+        // the first tiles' pages, codes and queries are all asked for before any is waited for
+        Carry st0, st1;
+        Pages p0, p1;
+        if (nt > 0) {
+            find(p0, 0);
+            find(p1, 1);
+            find(pg, 2);
+            th0 = load(st0, p0, 0);
+            if (keys) {
+                th1 = load(st1, p1, 1);
+                th2 = load(st, pg, 2);
+            } else {
+                th1 = load(st, p1, 1);
+            }
+        }
+        // the step before the first: no weight, but products with its values are taken
+        half8_t* before = &lds.v[4][0][0][0];
+        for (int x = threadIdx.x; x < 4 * D; x += WAVES * 64) before[x] = half8_t{};
+        unit_s = load_block_queries<FMT, D, WAVES>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, wave, lds.top, qf);
+        if (nt > 0) {
+            store(st0, 0, th0);
+            if (keys) {
+                store(st1, 1, th1);
+                find(pg, 3);
+            }
+        }
+    }
+    __syncthreads();
+    start(0);
+    if (nt > 0) e_ref = __builtin_amdgcn_readfirstlane(lds.e[0]);
+    __syncthreads();
+    for (int i = 0; i < nt; ++i) {
+        // Into what the last tile left: keys of tile i + 2, values of tile i + 1.  The two
+        // waves of a SIMD do so at different times, the one beside the other's products.
+        uint64_t next = 0;
+        if (keys) {
+            store(st, i + 2, th2);
+            next = load(st, pg, i + 3);
+            find(pg, i + 4);
+        }
+        // a tile that none of the wave's rows sees takes part with no weight
+        const int base = base_of(i);
+        const bool whole = (th0 == ~0ull) & wr.whole(base, kT);
+        uint64_t seen = ~0ull;
+        const uint32_t e = lds.e[(i + 1) & 3];
+        if (!whole) seen = seen_bits(a, q, qi, base, th0);
+        if (has_rows) attend(i, std::integral_constant<int, 0>{}, whole, seen);
+        if (!keys) {
+            store(st, i + 1, th1);
+            next = load(st, pg, i + 2);
+            find(pg, i + 3);
+        }
+        e_next = __builtin_amdgcn_readfirstlane(e);
+        if (has_rows) attend(i, std::integral_constant<int, 1>{}, whole, seen);
+        th0 = th1;
+        th1 = keys ? th2 : next;
+        th2 = next;
+        __syncthreads();
+    }
+
+    if (has_rows) finish(2 * nt - 1);
+    l += __shfl_xor(l, 32, 64);
+    if (!ok) return;
+    const float y0 = l == 0.0f ? 0.0f : __uint_as_float((e_ref + 1u) << 23) * L::UNIT / l;
+    const float ls = l == 0.0f ? -__builtin_inff() : __builtin_log2f(l) - nm;
+    constexpr int HI = 32 / M::LR, RUN = 4 * M::E;          // accumulator row m is lane m % LR, element HI d + m / LR
+#pragma unroll
+    for (int n = 0; n < 4 / HI; ++n) {
+        float y[RUN];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < M::E; ++e) y[j * M::E + e] = l == 0.0f ? 0.0f : o[e / HI][4 * (e % HI * 2 + n) + j] * y0;
+        const int64_t d = to * D + (8 * n + 4 * g) * M::E;
+        if (sp.splits > 1) {
+            float* p = po + (int64_t)split * a.tokens * a.q_heads * D + d;
+#pragma unroll
+            for (int e = 0; e < RUN; e += 4) *reinterpret_cast<float4_t*>(p + e) = float4_t{y[e], y[e + 1], y[e + 2], y[e + 3]};
+        } else {
+            store_out<RUN>(a, d, y);
+        }
+    }
+    if (g == 0) {
+        if (sp.splits > 1) pl[(int64_t)split * a.tokens * a.q_heads + to] = ls;
+        else if (a.lse) a.lse[to] = ls * 0x1.62e43p-1f;
+    }
+}
+
+}  // namespace
+
+const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, float* po, float* pl, hipStream_t s) {
+    const dim3 grid((unsigned)a.c.heads * row_blocks, (unsigned)sp.splits, (unsigned)a.batch);
+    for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
+        constexpr int W = D() == 256 ? 4 : 8;
+        k_kv_attn_many<FMT(), D(), W><<<grid, W * 64, 0, s>>>(a, sp, po, pl);
+    });
+    return kname("k_kv_attn_many", a.c.fmt, a.c.dim, a.c.dim == 256 ? 4 : 8);
+}
+
+}  // namespace bg
