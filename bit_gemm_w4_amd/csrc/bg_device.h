@@ -78,6 +78,36 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     return p;
 }
 
+// The scale of a unit and what its quotients v / s need: the codes are the
+// roundings of the correctly rounded binary32 quotient.  Rather than one
+// IEEE division per element (a long instruction sequence on this device), a
+// unit computes r = RN(1/s) once and each element takes Markstein's
+// correction of q0 = RN(v r): with the exact remainder e = v - q0 s (one
+// fma), RN(q0 + e r) is the correctly rounded quotient, since r is within
+// half an ulp of 1/s and q0 within one ulp of v/s (P. Markstein, IBM J. Res.
+// Dev. 34(1), 1990; the theorem holds without overflow or underflow).  Units
+// whose scale lies outside [2^-100, 2^100] (r could overflow, or the
+// remainder underflow) divide instead.
+struct QScale {
+    float s, r;
+    bool mk;
+};
+
+__device__ __forceinline__ void quotients8(const float v[8], const QScale& u, float d[8]) {
+    if (u.mk) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q0 = v[i] * u.r;
+            // (the sign is v's, as in v / s: -0 and quotients that round to
+            // zero stay negative)
+            d[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, u.s, v[i]), u.r, q0), v[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = v[i] / u.s;
+    }
+}
+
 // Wave-level reductions over groups of W lanes (W a power of two <= 64).
 template <int W>
 __device__ __forceinline__ float wave_max(float v) {

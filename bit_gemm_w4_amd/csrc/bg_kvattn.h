@@ -88,18 +88,6 @@ __device__ __forceinline__ KvRange kv_range(const KvAttnArgs& a, const KvSeq& q,
     return r;
 }
 
-// First row of the 16 tokens from position j (a multiple of 16) in the code and
-// record arrays.  Where the position's page does not exist, row 0 of the
-// cache, and bit s of `there` stays clear.
-__device__ __forceinline__ int64_t kv_run(const KvAttnArgs& a, const int32_t* table, int h, int j, uint32_t& there, int s) {
-    const int p = j >> a.c.page_shift;
-    int page = p < a.max_pages ? table[p] : -1;
-    const bool ok = page >= 0 && page < a.c.pages;
-    there |= (ok ? 1u : 0u) << s;
-    page = ok ? page : 0;
-    return (((int64_t)page * a.c.heads + h) << a.c.page_shift) + (ok ? j & ((1 << a.c.page_shift) - 1) : 0);
-}
-
 // How a 16-lane row group holds a row of codes: a key's D codes over 4 lanes,
 // KC chunks of KB bytes each; a value's over 16 lanes, VB bytes each.  Operands
 // hold UNIT^-1 times the code.

@@ -28,41 +28,11 @@ namespace bg {
 
 enum { G_TENSOR = 0, G_ROW = 1, G_ROW_G128 = 2, G_BLOCK128 = 3 };
 
-// The scale of a unit and what its quotients v / s need: the codes are the
-// roundings of the correctly rounded binary32 quotient.  Rather than one
-// IEEE division per element (a long instruction sequence on this device), a
-// unit computes r = RN(1/s) once and each element takes Markstein's
-// correction of q0 = RN(v r): with the exact remainder e = v - q0 s (one
-// fma), RN(q0 + e r) is the correctly rounded quotient, since r is within
-// half an ulp of 1/s and q0 within one ulp of v/s (P. Markstein, IBM J. Res.
-// Dev. 34(1), 1990; the theorem holds without overflow or underflow).  Units
-// whose scale lies outside [2^-100, 2^100] (r could overflow, or the
-// remainder underflow) divide instead.
-struct QScale {
-    float s, r;
-    bool mk;
-};
-
 template <bool FP8>
 __device__ __forceinline__ QScale unit_scale(float amax) {
     float s = amax / (FP8 ? 448.0f : 127.0f);
     s = s == 0.0f ? 1.0f : s;
     return QScale{s, 1.0f / s, s >= 0x1p-100f && s <= 0x1p100f};
-}
-
-__device__ __forceinline__ void quotients8(const float v[8], const QScale& u, float d[8]) {
-    if (u.mk) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q0 = v[i] * u.r;
-            // (the sign is v's, as in v / s: -0 and quotients that round to
-            // zero stay negative)
-            d[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, u.s, v[i]), u.r, q0), v[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = v[i] / u.s;
-    }
 }
 
 // Quantize 8 values with the unit's scale and store 8 bytes at q[idx].

@@ -11,6 +11,12 @@
 // (no LDS, no barrier in the loop), with the next 32 in flight:
 //   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' codes, B = 16 rows
 //   O^T += V^T P^T  the same instruction, A = 16 head elements of 32 tokens
+// The tile's pages are looked up two tiles ahead; 8 waves a CU with two tiles each
+// keep about 130 KB of codes in flight, and 8-bit caches stream at 5.2 TB/s (decode
+// of 32 x 8192 tokens, 554 MB: 106 us; a large copy runs at 4.8 TB/s).  4 bits
+// have half the bytes for the same instructions: 4 x 131072 tokens 571 MB in
+// 117 us, 4.9 TB/s, and a block's start (6 us) weighs more.
+//
 // The accumulator of S^T holds, in lane (row r, g), tokens 4 g .. 4 g + 3 of
 // each 16; those of two S^T tiles are exactly the 8 k-slots that lane feeds to
 // the second product if V's k-slots are numbered the same way, so the weights
@@ -24,7 +30,7 @@
 // fits (elements below 2^-38 of their row's largest lose bits).  Scales stay in
 // binary32: the key's on the score, the value's on the weight.  The weight times
 // the value's scale, relative to the largest so far of each, is what is rounded
-// to FP16 for the second product: 2^-12 at most, against 2^-9 for BF16.  The
+// to FP16 for the second product: off by 2^-11 at most, against 2^-8 for BF16.  The
 // reference maximum of a row moves only when a score passes it by 2^8 (weights
 // reach 256 at most), so in the steady state a tile needs no lane exchange.
 #include "bg_device.h"
@@ -47,11 +53,15 @@ struct Tile {
     uint32_t kz[2];          // 4-bit: the record of the token whose key this lane holds
     uint32_t there;          // bit s: 16 tokens s lie in a page that exists
 
-    __device__ __forceinline__ void load(const KvAttnArgs& a, const int32_t* table, int h, int tile, int r, int g) {
+    // page: those of the tile's two halves.
+    __device__ __forceinline__ void load(const KvAttnArgs& a, const int (&page)[2], int h, int tile, int r, int g) {
         there = 0;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int64_t run = kv_run(a, table, h, tile * 32 + 16 * s, there, s);
+            const bool ok = page[s] >= 0 && page[s] < a.c.pages;
+            there |= (ok ? 1u : 0u) << s;
+            const int in = (tile * 32 + 16 * s) & ((1 << a.c.page_shift) - 1);
+            const int64_t run = ok ? (((int64_t)page[s] * a.c.heads + h) << a.c.page_shift) + in : 0;
             const uint8_t* kp = a.c.k + run * L::ROW;
             const uint8_t* vp = a.c.v + run * L::ROW;
 #pragma unroll
@@ -69,7 +79,7 @@ struct Tile {
 
 // RT row tiles of 16 rows per wave.
 template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(kWaves * 64) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+__global__ void __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 2 : 1) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     constexpr int DT = D / 16, ST = D / 32, PAD = D + 4;
     __shared__ float o_lds[kWaves][16][PAD];
@@ -92,6 +102,22 @@ __global__ void __launch_bounds__(kWaves * 64) k_kv_attn_few(KvAttnArgs a, KvSpl
             pl[((int64_t)split * a.tokens + q.q0 + row / G) * a.q_heads + h * G + row % G] = -__builtin_inff();
         }
         return;
+    }
+
+    // a tile's pages are looked up two tiles before its codes are asked for
+    auto find = [&](int (&page)[2], int i) {
+        const int base = rg.tile(i < t1 ? i : t1 - 1) * 32;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int64_t p = (base + 16 * s) >> a.c.page_shift;
+            page[s] = table[p < a.max_pages ? p : a.max_pages - 1];     // past the table: past the sequence, masked
+        }
+    };
+    int pa[2] = {}, pb[2] = {};
+    int i = t0 + wave;
+    if (t0 < t1) {
+        find(pa, i);
+        find(pb, i + kWaves);
     }
 
     half8_t qf[RT][ST];
@@ -222,13 +248,17 @@ __global__ void __launch_bounds__(kWaves * 64) k_kv_attn_few(KvAttnArgs a, KvSpl
     };
 
     Tile<FMT, D> ta, tb;
-    int i = t0 + wave;
-    if (i < t1) ta.load(a, table, h, rg.tile(i), r, g);
+    if (i < t1) {
+        ta.load(a, pa, h, rg.tile(i), r, g);
+        find(pa, i + 2 * kWaves);
+    }
     for (; i < t1; i += 2 * kWaves) {
-        if (i + kWaves < t1) tb.load(a, table, h, rg.tile(i + kWaves), r, g);
+        if (i + kWaves < t1) tb.load(a, pb, h, rg.tile(i + kWaves), r, g);
+        find(pb, i + 3 * kWaves);
         compute(ta, rg.tile(i));
         if (i + kWaves >= t1) break;
-        if (i + 2 * kWaves < t1) ta.load(a, table, h, rg.tile(i + 2 * kWaves), r, g);
+        if (i + 2 * kWaves < t1) ta.load(a, pa, h, rg.tile(i + 2 * kWaves), r, g);
+        find(pa, i + 4 * kWaves);
         compute(tb, rg.tile(i + kWaves));
     }
 
@@ -298,36 +328,60 @@ __global__ void __launch_bounds__(kWaves * 64) k_kv_attn_few(KvAttnArgs a, KvSpl
 }
 
 // Joins the splits of a row: o = sum_s 2^(ls_s - max) o_s / sum_s 2^(ls_s - max).
-// One wave per row; lane s holds split s's weight (64 at a time).
-template <int D>
+// WPR waves take a row's splits in turn (64 splits one after the other: 18 us), eight
+// partials in flight each.  A split without tokens wrote no partial: its weight is 0
+// and what lies there is not used.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, const float* po, const float* pl) {
-    const int lane = threadIdx.x & 63, b = blockIdx.y;
+    __shared__ float part[WPR == 1 ? 1 : 4][D];
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.y;
     const KvSeq q = kv_seq(a, b);
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= (int64_t)q.len * a.q_heads) return;
-    const int64_t to = q.q0 * a.q_heads + row, n = a.tokens * a.q_heads;
+    const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
+    const bool there = row < (int64_t)q.len * a.q_heads;
+    if (WPR == 1 && !there) return;
+    const int64_t to = q.q0 * a.q_heads + (there ? row : 0), n = a.tokens * a.q_heads;
     float top = -__builtin_inff();
-    for (int s = lane; s < splits; s += 64) top = __builtin_fmaxf(top, pl[s * n + to]);
+    if (there)
+        for (int s = lane; s < splits; s += 64) top = __builtin_fmaxf(top, pl[s * n + to]);
     top = wave_max<64>(top);
     const float base = top == -__builtin_inff() ? 0.0f : top;
-    float y[D / 64] = {}, sum = 0.0f;
+    float y[E] = {}, sum = 0.0f;
     for (int s0 = 0; s0 < splits; s0 += 64) {
-        const float ls = s0 + lane < splits ? pl[(s0 + lane) * n + to] : -__builtin_inff();
+        const float ls = there && s0 + lane < splits ? pl[(s0 + lane) * n + to] : -__builtin_inff();
         const float w = __builtin_amdgcn_exp2f(ls - base);
         sum += w;
         const int last = splits - s0 < 64 ? splits - s0 : 64;
-        for (int s = 0; s < last; ++s) {
-            const float ws = __shfl(w, s, 64);
-            if (ws == 0.0f) continue;     // a split without tokens wrote no partial
-            const float* p = po + ((int64_t)(s0 + s) * n + to) * D + lane * (D / 64);
+        for (int s = wave % WPR; s < last; s += 8 * WPR) {
+            float p[8][E], ws[8];
 #pragma unroll
-            for (int d = 0; d < D / 64; ++d) y[d] += ws * p[d];
+            for (int x = 0; x < 8; ++x) {
+                const int sx = s + x * WPR < last ? s + x * WPR : s;
+                ws[x] = s + x * WPR < last ? __shfl(w, sx, 64) : 0.0f;
+                const float* at = po + ((int64_t)(s0 + sx) * n + to) * D + lane * E;
+#pragma unroll
+                for (int d = 0; d < E; ++d) p[x][d] = at[d];
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int d = 0; d < E; ++d) y[d] += ws[x] == 0.0f ? 0.0f : ws[x] * p[x][d];
         }
     }
     sum = wave_sum<64>(sum);
+    if constexpr (WPR > 1) {
 #pragma unroll
-    for (int d = 0; d < D / 64; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] / sum;
-    store_out<D / 64>(a, to * D + lane * (D / 64), y);
+        for (int d = 0; d < E; ++d) part[wave][lane * E + d] = y[d];
+        __syncthreads();
+        if (wave > 0 || !there) return;
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+#pragma unroll
+            for (int d = 0; d < E; ++d) y[d] += part[w][lane * E + d];
+    }
+#pragma unroll
+    for (int d = 0; d < E; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] / sum;
+    store_out<E>(a, to * D + lane * E, y);
     if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
 }
 
@@ -358,7 +412,9 @@ Plan plan_of(const KvAttnArgs& a) {
     const int64_t blocks = a.batch * a.c.heads * p.row_blocks;
     // Many rows: one block a CU and one round of them, a block's start being worth four
     // tiles (64-row trees over 16 x 8192 tokens: 193 us with 256 blocks, 204 with 512).
-    int64_t splits = ((p.many ? 256 : 1024) + blocks - 1) / blocks;
+    // Few rows: two, again one round (decode of 32 x 8192 tokens, E4M3: 85 us with 512
+    // blocks, 88 with 1,024; 64 x 4,096 in a window, INT8: 55 against 69).
+    int64_t splits = ((p.many ? 256 : 512) + blocks - 1) / blocks;
     const int64_t most = (tiles + 7) / 8;
     splits = splits > most ? most : splits;
     splits = splits > 256 ? 256 : splits < 1 ? 1 : splits;
@@ -386,10 +442,15 @@ const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
         else if constexpr (D() != 256) k_kv_attn_few<FMT(), D(), 2><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
     });
     if (p.sp.splits > 1) {
-        const dim3 join((unsigned)((a.max_q * a.q_heads + 3) / 4), (unsigned)a.batch);
-        if (a.c.dim == 64) k_kv_attn_join<64><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
-        else if (a.c.dim == 128) k_kv_attn_join<128><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
-        else k_kv_attn_join<256><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+        const bool wide = p.sp.splits > 8;
+        const dim3 join((unsigned)(wide ? a.max_q * a.q_heads : (a.max_q * a.q_heads + 3) / 4), (unsigned)a.batch);
+        auto go = [&](auto D) {
+            if (wide) k_kv_attn_join<D(), 4><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+            else k_kv_attn_join<D(), 1><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+        };
+        if (a.c.dim == 64) go(std::integral_constant<int, 64>{});
+        else if (a.c.dim == 128) go(std::integral_constant<int, 128>{});
+        else go(std::integral_constant<int, 256>{});
     }
     return name ? name : kname("k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
 }

@@ -543,6 +543,12 @@ def _on_device(fn: str, cache: KVCache, *tensors):
         raise ValueError(f"{fn}: the cache is on {cache.device}, the current device is {torch.cuda.current_device()}")
 
 
+def _raw_stream(device: int) -> int:
+    """The handle of the device's current stream (without the Stream object of
+    torch.cuda.current_stream(), which costs a call of a few microseconds more)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _on_stream(stream, tensors, call):
     """call() with `stream` current, so what it allocates belongs to that stream;
     the operands' memory is kept from reuse until the stream has passed."""
@@ -583,7 +589,7 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torc
         raise ValueError(f"{fn}: the last axis of k and v must be contiguous")
     _on_device(fn, cache, k, v, slots)
     _check(lib().kv_cache_write(cache.address, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt,
-                                slots.data_ptr(), T, torch.cuda.current_stream().cuda_stream), fn)
+                                slots.data_ptr(), T, _raw_stream(cache.device.index)), fn)
 
 
 def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None):
@@ -601,7 +607,7 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torc
     k, v = (torch.empty((T, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device) for _ in range(2))
     if T:
         _check(lib().kv_cache_read(cache.address, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), dt,
-                                   torch.cuda.current_stream().cuda_stream), fn)
+                                   _raw_stream(cache.device.index)), fn)
     return k, v
 
 
@@ -649,7 +655,7 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
         return out
     _on_device(fn, cache, q, block_table, kv_lens, cu_q, tree, out, lse, ws)
     L = lib()
-    s = torch.cuda.current_stream().cuda_stream
+    s = _raw_stream(cache.device.index)
     args = _KV_ATTN.pack(
         cache.address, q.data_ptr(), q.stride(0), q.stride(1), block_table.data_ptr(), max_pages, kv_lens.data_ptr(),
         0 if cu_q is None else cu_q.data_ptr(), 0 if tree is None else tree.data_ptr(), out.data_ptr(),
