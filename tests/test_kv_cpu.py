@@ -188,3 +188,32 @@ def test_reference_masks():
     see = ref.visible(3, 5, np.array([1, 1, 0, 1, 1], bool), tree=[1, 0b11, 0b101])
     assert [list(np.flatnonzero(r)) for r in see] == [[0, 1], [0, 1, 3], [0, 1, 4]]
     assert not ref.visible(4, 2, np.ones(2, bool))[:2].any()
+
+
+def test_tree_bits():
+    from bit_gemm_w4_amd.attention_layer import tree_bits
+    assert tree_bits([-1, 0, 0, 2, -1]) == [[1], [3], [5], [13], [16]]
+    chain = tree_bits([i - 1 for i in range(70)])
+    assert chain[63] == [-1, 0] and chain[69] == [-1, 63] and chain[62] == [(1 << 63) - 1, 0]
+    with pytest.raises(ValueError, match="parent"):
+        tree_bits([-1, 1])
+
+
+def test_tokens_times_heads_are_bounded(L):
+    c = cache(kv_heads=1)
+    a = attn(c, tokens=1 << 20, q_heads=512, cu_q=P)
+    assert L.kv_attn(ctypes.addressof(a), P, 1 << 40, None) == E_SHAPE
+
+
+def test_workspace_follows_the_split(L):
+    """Many rows of a short sequence, or more blocks than the device holds at once, need none; it grows with neither pages nor window alone."""
+    c = cache(pages=100000, kv_heads=8)
+
+    def need(**kw):
+        a = attn(c, **{**dict(q_heads=32, max_pages=8192), **kw})
+        return L.kv_attn_workspace_bytes(ctypes.addressof(a))
+    assert need(tokens=64, batch=64, max_q=1, max_kv=200) == 0
+    assert need(tokens=4096, batch=1, max_q=4096, max_kv=65536) == 0
+    one = need(tokens=1, batch=1, max_q=1, max_kv=131072)
+    assert one > 0 and one % (32 * 129 * 4) == 0
+    assert need(tokens=1, batch=1, max_q=1, max_kv=131072, window=4096) < one
