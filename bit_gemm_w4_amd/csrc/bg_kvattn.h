@@ -210,106 +210,133 @@ __device__ __forceinline__ half8_t value_fragment(const uint32_t (&v)[8][VW], co
     return join4(x[0], x[1], x[2], x[3]);
 }
 
-// The row's query fragments for lane group g of GROUPS, scaled by a power of
+typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+
+// The larger of each half's magnitude, as bits (the order of FP16's and of BF16's).
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a), __builtin_bit_cast(ushort2_t, b & 0x7FFF7FFFu)));
+}
+
+__device__ __forceinline__ uint32_t max_magnitude(uint4 x) {
+    return max_magnitude(max_magnitude(max_magnitude(max_magnitude(0u, x.x), x.y), x.z), x.w);
+}
+
+// The exponent e of the largest of BF16 magnitudes (the larger half of m), at least
+// -100; 13, which leaves them as they are, if that is 0 or not finite.
+__device__ __forceinline__ int scale_exponent(uint32_t m) {
+    const uint32_t top = m >> 16 > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu;
+    const int e = (int)(top >> 7) - 127;
+    return top == 0u || e == 128 ? 13 : e < -100 ? -100 : e;
+}
+
+// Eight query elements as an FP16 fragment, BF16 ones times `up` (FP16 ones are exact as
+// they are), in the order of the format's codes.
+template <int FMT>
+__device__ __forceinline__ half8_t query8(bool bf16, uint4 x, float up) {
+    half2_t y[4];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (bf16) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) y[n] = half2_t{(_Float16)(__uint_as_float(w[n] << 16) * up), (_Float16)(__uint_as_float(w[n] & 0xFFFF0000u) * up)};
+    } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) y[n] = __builtin_bit_cast(half2_t, w[n]);
+    }
+    return FMT == KV_U4 ? half8_t{y[0][0], y[2][0], y[0][1], y[2][1], y[1][0], y[3][0], y[1][1], y[3][1]} : join4(y[0], y[1], y[2], y[3]);
+}
+
+// The factor that takes a product of operands to a base-2 exponent, queries scaled so
+// that 2^e comes to 2^13.
+template <int FMT, int D>
+__device__ __forceinline__ float query_unit(const KvAttnArgs& a, int e) {
+    return a.scale * 0x1.715476p0f * KvLayout<FMT, D>::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+}
+
+// The row's query fragments for lane group g of GROUPS, BF16 ones scaled by a power of
 // two so that FP16 holds them; returns the factor that takes a product of
 // operands to a base-2 exponent.  Rows that are not there are zeros.
 template <int FMT, int D, int GROUPS>
 __device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int g, bool ok, half8_t* f) {
     using L = KvLayout<FMT, D>;
     constexpr int N = D / (8 * GROUPS), CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;    // elements a lane holds in a run
-    uint32_t w[N][4];
-    float top = 0.0f;
+    uint4 w[N];
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int in = i * 8 % CHUNK, c = i * 8 / CHUNK;
         const int d = c * GROUPS * CHUNK + g * CHUNK + in;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (ok) x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
-        w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const float lo = a.bf16 ? __uint_as_float(w[i][n] << 16) : f16_to_f32(w[i][n] & 0xFFFFu);
-            const float hi = a.bf16 ? __uint_as_float(w[i][n] & 0xFFFF0000u) : f16_to_f32(w[i][n] >> 16);
-            top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf(lo), __builtin_fabsf(hi)));
-        }
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (ok) w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
     }
+    int e = 13;
+    if (a.bf16) {
 #pragma unroll
-    for (int o = 64 / GROUPS; o < 64; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
-    int e = (int)(__float_as_uint(top) >> 23) - 127;      // top in [2^e, 2^(e + 1))
-    if (e == 128 || top == 0.0f) e = 13;                   // infinities stay, and zeros
-    e = e < -100 ? -100 : e;
+        for (int i = 0; i < N; ++i) top = max_magnitude(top, max_magnitude(w[i]));
+#pragma unroll
+        for (int o = 64 / GROUPS; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        e = scale_exponent(top);
+    }
     const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        _Float16 y[8];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const float lo = a.bf16 ? __uint_as_float(w[i][n] << 16) : f16_to_f32(w[i][n] & 0xFFFFu);
-            const float hi = a.bf16 ? __uint_as_float(w[i][n] & 0xFFFF0000u) : f16_to_f32(w[i][n] >> 16);
-            y[2 * n] = (_Float16)(lo * up);
-            y[2 * n + 1] = (_Float16)(hi * up);
-        }
-        f[i] = FMT == KV_U4 ? half8_t{y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]}
-                            : half8_t{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
-    }
-    return a.scale * 0x1.715476p0f * L::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+    for (int i = 0; i < N; ++i) f[i] = query8<FMT>(a.bf16, w[i], up);
+    return query_unit<FMT, D>(a, e);
 }
 
-// The same for a block of WAVES waves of 32 rows, two lane groups, in fragments of 8
-// elements c = 0 .. D / 16 - 1 that follow the keys' order (fragment 4 i + n of a
-// key is the i-th of lane group n), scaled by one power of two: the largest finite element of
-// all its rows lands in [2^13, 2^14).
-template <int FMT, int D, int WAVES>
-__device__ __forceinline__ float load_block_queries(const KvAttnArgs& a, int64_t at, int g, bool ok, int wave, float* lds, half8_t* f) {
+// The same for a wave of 32 rows, two lane groups, in fragments of 8 elements
+// c = 0 .. D / 16 - 1 that follow the keys' order (fragment 4 i + n of a key is the
+// i-th of lane group n), as they lie in memory.
+template <int FMT, int D>
+__device__ __forceinline__ void load_queries(const KvAttnArgs& a, int64_t at, int g, bool ok, half8_t* f) {
     using L = KvLayout<FMT, D>;
-    constexpr int N = D / 16, CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;
-    float top = 0.0f;
-    auto pair = [&](uint32_t w, float& lo, float& hi) {
-        lo = a.bf16 ? __uint_as_float(w << 16) : f16_to_f32(w & 0xFFFFu);
-        hi = a.bf16 ? __uint_as_float(w & 0xFFFF0000u) : f16_to_f32(w >> 16);
-    };
+    constexpr int CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
+    for (int c = 0; c < D / 16; ++c) {
         const int i = c >> 1, n = 2 * (c & 1) + g;
         const int d = i * 8 / CHUNK * 4 * CHUNK + n * CHUNK + i * 8 % CHUNK;
         uint4 y = make_uint4(0, 0, 0, 0);
         if (ok) y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            pair(w[k], lo, hi);
-            lo = __builtin_fabsf(lo);
-            hi = __builtin_fabsf(hi);
-            top = __builtin_fmaxf(top, lo < __builtin_inff() ? lo : 0.0f);
-            top = __builtin_fmaxf(top, hi < __builtin_inff() ? hi : 0.0f);
-        }
         f[c] = __builtin_bit_cast(half8_t, y);
     }
-    top = wave_max<64>(top);
-    if ((threadIdx.x & 63) == 0) lds[wave] = top;
-    __syncthreads();
+}
+
+// ... and to FP16, BF16 ones scaled by one power of two for the block of WAVES waves: its
+// largest element that is finite lands in [2^13, 2^14).
+template <int FMT, int D, int WAVES>
+__device__ __forceinline__ float scale_queries(const KvAttnArgs& a, int wave, uint32_t* lds, half8_t* f) {
+    constexpr int N = D / 16;
+    int e = 13;
+    if (a.bf16) {
+        uint32_t top = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = __builtin_fmaxf(top, lds[w]);
-    int e = top == 0.0f ? 13 : (int)(__float_as_uint(top) >> 23) - 127;
-    e = __builtin_amdgcn_readfirstlane(e < -100 ? -100 : e);
+        for (int c = 0; c < N; ++c) top = max_magnitude(top, max_magnitude(__builtin_bit_cast(uint4, f[c])));
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        if (__any((top >> 16) >= 0x7F80u || (top & 0xFFFFu) >= 0x7F80u)) {
+            // infinities or NaN: the largest of the others
+            top = 0;
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                const uint4 v = __builtin_bit_cast(uint4, f[c]);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t lo = w[k] & 0x7FFFu, hi = w[k] >> 16 & 0x7FFFu;
+                    top = max_magnitude(top, (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F80u ? hi : 0u) << 16);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        }
+        if ((threadIdx.x & 63) == 0) lds[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) top = max_magnitude(top, lds[w]);
+        e = __builtin_amdgcn_readfirstlane(scale_exponent(top));
+    }
     const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-        const uint4 v = __builtin_bit_cast(uint4, f[c]);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        _Float16 y[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            pair(w[k], lo, hi);
-            y[2 * k] = (_Float16)(lo * up);
-            y[2 * k + 1] = (_Float16)(hi * up);
-        }
-        f[c] = FMT == KV_U4 ? half8_t{y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]}
-                            : half8_t{y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
-    }
-    return a.scale * 0x1.715476p0f * L::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+    for (int c = 0; c < N; ++c) f[c] = query8<FMT>(a.bf16, __builtin_bit_cast(uint4, f[c]), up);
+    return query_unit<FMT, D>(a, e);
 }
 
 template <int N>
@@ -319,10 +346,13 @@ __device__ __forceinline__ void store_out(const KvAttnArgs& a, int64_t at, const
         *p = a.bf16 ? f32_to_bf16(y[0]) : f32_to_f16(y[0]);
     } else {
         uint32_t w[N / 2];
+        if (a.bf16) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i)
-            w[i] = a.bf16 ? (uint32_t)f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16
-                          : (uint32_t)f32_to_f16(y[2 * i]) | (uint32_t)f32_to_f16(y[2 * i + 1]) << 16;
+            for (int i = 0; i < N / 2; ++i) w[i] = (uint32_t)f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) w[i] = (uint32_t)f32_to_f16(y[2 * i]) | (uint32_t)f32_to_f16(y[2 * i + 1]) << 16;
+        }
         if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
         else if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         else {

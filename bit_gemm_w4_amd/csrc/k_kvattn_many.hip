@@ -22,7 +22,7 @@
 //   (two chains that do not wait for one another), with this step's weights in the
 //   vector units' slots between them.
 // A tile of 64 positions takes a block about 2.0 us (4,300 cycles, 2,048 of them in
-// each SIMD's matrix core); a block's start (pages, first codes, queries) 8 us, so
+// each SIMD's matrix core); a block's start (pages, first codes, queries) 6 us, so
 // blocks are made as few as fill the device once.  2,048 queries over a window
 // of 4,096 in E4M3 (8 kv heads of 4, D = 128): 185 us, 742 TFLOP/s; the few-row
 // kernel takes 460 us.
@@ -59,7 +59,7 @@ struct ManyLds {
     half8_t v[VRING][2][2][D];        // [step mod VRING][16 tokens][lane half][element e of lane r at e LR + r]
     float ks[4][kT], vs[4][kT];       // [tile mod 4]: key scales times the queries' unit, value scales over 2^(e - 126)
     uint32_t e[4];                    // [tile mod 4]
-    float top[8];
+    uint32_t top[8];
 };
 
 // Where a sequence's tokens of one head lie.
@@ -402,6 +402,9 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
             find(p0, 0);
             find(p1, 1);
             find(pg, 2);
+        }
+        load_queries<FMT, D>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, qf);
+        if (nt > 0) {
             th0 = load(st0, p0, 0);
             if (keys) {
                 th1 = load(st1, p1, 1);
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
         // the step before the first: no weight, but products with its values are taken
         half8_t* before = &lds.v[4][0][0][0];
         for (int x = threadIdx.x; x < 4 * D; x += WAVES * 64) before[x] = half8_t{};
-        unit_s = load_block_queries<FMT, D, WAVES>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, wave, lds.top, qf);
+        unit_s = scale_queries<FMT, D, WAVES>(a, wave, lds.top, qf);
         if (nt > 0) {
             store(st0, 0, th0);
             if (keys) {
