@@ -102,7 +102,12 @@ struct KvLayout {
 
 template <int N>
 __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* w) {
-    if constexpr (N == 2) {
+    if constexpr (N == 32) {
+        load_bytes<16>(p, w);
+        load_bytes<16>(p + 16, w + 4);
+    } else if constexpr (N == 1) {
+        w[0] = *p;
+    } else if constexpr (N == 2) {
         w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else if constexpr (N == 4) {
         w[0] = *reinterpret_cast<const uint32_t*>(p);
@@ -282,19 +287,14 @@ __device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int
     return query_unit<FMT, D>(a, e);
 }
 
-// The same for a wave of 32 rows, two lane groups, in fragments of 8 elements
-// c = 0 .. D / 16 - 1 that follow the keys' order (fragment 4 i + n of a key is the
-// i-th of lane group n), as they lie in memory.
-template <int FMT, int D>
+// A wave's 32 rows, two lane groups, as they lie in memory: fragment c is elements
+// 16 c + 8 g .. 16 c + 8 g + 7.
+template <int D>
 __device__ __forceinline__ void load_queries(const KvAttnArgs& a, int64_t at, int g, bool ok, half8_t* f) {
-    using L = KvLayout<FMT, D>;
-    constexpr int CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-        const int i = c >> 1, n = 2 * (c & 1) + g;
-        const int d = i * 8 / CHUNK * 4 * CHUNK + n * CHUNK + i * 8 % CHUNK;
         uint4 y = make_uint4(0, 0, 0, 0);
-        if (ok) y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
+        if (ok) y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + 16 * c + 8 * g);
         f[c] = __builtin_bit_cast(half8_t, y);
     }
 }

@@ -409,15 +409,27 @@ Plan plan_of(const KvAttnArgs& a) {
         seen = most < seen ? most : seen;
     }
     const int64_t tiles = (seen + tile - 1) / tile > 0 ? (seen + tile - 1) / tile : 1;
+    // The number of splits that takes the least time by this model: rounds of the blocks
+    // that the device holds at once, each a start and its tiles; the join; and the
+    // partials' way to memory and back at 4 TB/s.  Many rows: one block a CU, a tile
+    // 2.1 us, a start worth 3.  Few: two blocks a CU (one where registers fill it), each
+    // wave a quarter of the tiles, 2 us each, a start worth 2.  As many splits as fill the
+    // device, for which this stands, ran 136 blocks of 16 tiles as two rounds of 8 tiles in
+    // 94 us (one of 16: 58), and 35 sequences of 11687 tokens, D = 256, in 64 (47).
     const int64_t blocks = a.batch * a.c.heads * p.row_blocks;
-    // Many rows: one block a CU and one round of them, a block's start being worth four
-    // tiles (64-row trees over 16 x 8192 tokens: 193 us with 256 blocks, 204 with 512).
-    // Few rows: two, again one round (decode of 32 x 8192 tokens, E4M3: 85 us with 512
-    // blocks, 88 with 1,024; 64 x 4,096 in a window, INT8: 55 against 69).
-    int64_t splits = ((p.many ? 256 : 512) + blocks - 1) / blocks;
-    const int64_t most = (tiles + 7) / 8;
-    splits = splits > most ? most : splits;
-    splits = splits > 256 ? 256 : splits < 1 ? 1 : splits;
+    const int64_t room = p.many || a.c.dim == 256 || (p.rt == 2 && a.c.dim == 128) ? 256 : 512;
+    const double partials = (double)(a.tokens * a.q_heads * a.c.dim) * 8.0 / 4.0e6 / 2.0;
+    int64_t splits = 1;
+    double best = 1e30;
+    for (int64_t s = 1; s <= 256 && s <= tiles; ++s) {
+        const double run = (double)((tiles + s - 1) / s), rounds = (double)((blocks * s + room - 1) / room);
+        const double cost = rounds * (p.many ? 3.0 + run : 2.0 + (double)(((int64_t)run + 3) / 4)) + (s == 1 ? 0.0 : (p.many ? 2.0 : 1.5) + s * (partials + 1.0 / 64.0));
+        if (cost < best) {
+            best = cost;
+            splits = s;
+        }
+        if (blocks * s > 4 * room) break;
+    }
     p.sp.tiles = (int)((tiles + splits - 1) / splits);
     p.sp.splits = (int)((tiles + p.sp.tiles - 1) / p.sp.tiles);
     return p;

@@ -8,24 +8,23 @@
 //   O^T += V^T P^T  A = 32 head elements of 16 tokens, B = the weights in place
 // (the k-slots of V are numbered as the accumulator of S^T holds its tokens).
 // 32x32x16 and not 16x16x32: beside the latter's 16-cycle products the vector
-// units issue little (16 products with 4 multiply-adds and an exponential
-// between each: 478 ns of two waves, against 433 ns for the products alone; the
-// same work in 16x16x32: 844 ns).
+// units issue little (16 products with 4 multiply-adds after each: 444 ns of two
+// waves, against 433 ns for the products alone; the same work in 16x16x32: 658 ns).
 //
 // What else there is to do runs beside the products:
 // * A tile's codes turn to FP16 once per block, in LDS, as the fragments that the
 //   waves' products take (16 bytes per lane, contiguous over lanes: no bank
-//   conflicts in either direction).  Four waves carry keys, two tiles ahead, four
-//   values, one ahead; one barrier a tile.  The two waves of a SIMD carry at
-//   different times: the values' after the first of a tile's two steps.
+//   conflicts in either direction).  Each wave carries an eighth of a tile, keys two
+//   tiles ahead and values one, between its products; one barrier a tile.
 // * The products of the next step's scores and of the last step's values alternate
 //   (two chains that do not wait for one another), with this step's weights in the
 //   vector units' slots between them.
-// A tile of 64 positions takes a block about 2.0 us (4,300 cycles, 2,048 of them in
-// each SIMD's matrix core); a block's start (pages, first codes, queries) 6 us, so
-// blocks are made as few as fill the device once.  2,048 queries over a window
-// of 4,096 in E4M3 (8 kv heads of 4, D = 128): 185 us, 742 TFLOP/s; the few-row
-// kernel takes 460 us.
+// A tile of 64 positions takes a block 2.1 us (4,200 cycles, 2,048 of them in each SIMD's
+// matrix core); a block's start (pages, first codes, queries) 6 us.  2,048 queries
+// over a window of 4,096 in E4M3 (8 kv heads of 4, D = 128): 171 us, 806 TFLOP/s; the
+// few-row kernel takes 460 us, a library product of 8192^3 in FP16 runs at 1,064
+// TFLOP/s.  In 16x16x32, a barrier and codes of a tile at a time: 245 us; with half of
+// the waves carrying keys and half values outside the products: 175 us.
 //
 // Numerics as in the few-row kernel: codes exact in FP16, scales and statistics
 // in binary32.  Two things differ, both to spare vector instructions.  Queries are
@@ -44,22 +43,23 @@ namespace {
 
 constexpr int kT = 64, kRows = 32;          // positions of a tile, rows of a wave
 
-// Sixteen lanes' or 32 lanes' worth of a value row: VB bytes and E elements a lane.
+// A lane's part of a key row (KB bytes) and of a value row (VB bytes, E elements; LR lanes).
 template <int FMT, int D>
 struct ManyLayout {
-    using L = KvLayout<FMT, D>;
-    static constexpr int LR = L::ROW >= 64 ? 32 : 16;
-    static constexpr int VB = L::ROW / LR, VW = VB < 4 ? 1 : VB / 4, E = VB * L::PER;
+    static constexpr int ROW = KvLayout<FMT, D>::ROW, PER = KvLayout<FMT, D>::PER;
+    static constexpr int KB = ROW / 8, KW = KB / 4, KF = D / 64;               // bytes, words, fragments
+    static constexpr int VB = ROW >= 64 ? ROW / 64 : 1, E = VB * PER, LR = D / E;
 };
 
 template <int FMT, int D>
 struct ManyLds {
-    static constexpr int KRING = D == 256 ? 4 : 5, VRING = 5;
+    static constexpr int KRING = D == 256 ? 4 : 8, VRING = D == 256 ? 5 : 8;       // of 5 and 6 needed at D <= 128, 8 cost no division
     half8_t k[KRING][D / 8][32];      // [step mod KRING][8 elements][token]
     half8_t v[VRING][2][2][D];        // [step mod VRING][16 tokens][lane half][element e of lane r at e LR + r]
     float ks[4][kT], vs[4][kT];       // [tile mod 4]: key scales times the queries' unit, value scales over 2^(e - 126)
     uint32_t e[4];                    // [tile mod 4]
     uint32_t top[8];
+    uint16_t vz[4][kT];               // 4 bits: -2^-9 times the zero-points of values, FP16
 };
 
 // Where a sequence's tokens of one head lie.
@@ -80,70 +80,6 @@ struct ManyPages {
     // Offset in an array of `unit` bytes per token and head (in page 0 if the page does not exist); a page's bytes fit 32 bits.
     __device__ __forceinline__ uint64_t at(uint32_t page, int position, uint32_t unit) const {
         return (uint64_t)(there(page) ? page : 0u) * (rows * unit) + (row + (uint32_t)(position & ((1 << shift) - 1))) * unit;
-    }
-};
-
-// Sixteen tokens' keys or values on their way from memory to LDS.
-template <int FMT, int D>
-struct ManyStage {
-    using L = KvLayout<FMT, D>;
-    using M = ManyLayout<FMT, D>;
-    static constexpr int W = L::KW > 8 * M::VW ? L::KW : 8 * M::VW;
-    uint32_t c[W], z[FMT == KV_U4 ? 8 : 1];
-
-    // The 16 tokens from position `first`, of page `page`.
-    __device__ __forceinline__ void load_keys(const KvAttnArgs& a, const ManyPages& p, uint32_t page, int first, int lane) {
-        const uint8_t* kp = a.c.k + (p.at(page, first, L::ROW) + (uint32_t)((lane & 15) * L::ROW + (lane >> 4) * L::KB));
-#pragma unroll
-        for (int i = 0; i < L::KC; ++i) load_bytes<L::KB>(kp + i * 4 * L::KB, &c[i * (L::KB / 4)]);
-        if constexpr (FMT == KV_U4) load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + (p.at(page, first, 4) + 4 * (lane & 15)), z);
-    }
-    __device__ __forceinline__ void store_keys(half8_t (&t)[D / 8][32], int s, int lane) {
-        half8_t f[D / 32];
-        key_fragments<FMT, D>(c, z[0], f);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) t[4 * i + (lane >> 4)][16 * s + (lane & 15)] = f[i];
-    }
-
-    // A lane's 8 k-slots: tokens 4 half .. + 3 and 8 + 4 half .. + 3.
-    __device__ __forceinline__ void load_values(const KvAttnArgs& a, const ManyPages& p, uint32_t page, int first, int lane) {
-        const int half = lane >> 5, r = lane & (M::LR - 1);
-        const uint8_t* vp = a.c.v + (p.at(page, first, L::ROW) + (uint32_t)(4 * half * L::ROW + r * M::VB));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) load_bytes<M::VB>(vp + ((j & 3) + 8 * (j >> 2)) * L::ROW, &c[j * M::VW]);
-        if constexpr (FMT == KV_U4) {
-            const uint8_t* zp = reinterpret_cast<const uint8_t*>(a.c.vs) + (p.at(page, first, 4) + 16 * half);
-            load_bytes<16>(zp, z);
-            load_bytes<16>(zp + 32, z + 4);
-        }
-    }
-    __device__ __forceinline__ void store_values(half8_t (&t)[2][D], const KvRange& rg, int first, bool there, bool whole, int lane) {
-        const int half = lane >> 5, r = lane & 31;
-        uint32_t v[8][M::VW];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int n = 0; n < M::VW; ++n) v[j][n] = c[j * M::VW + n];
-        if (!whole) {
-            // what no row sees may hold anything: its value becomes 0
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool live = there & rg.live(first + 4 * half + (j & 3) + 8 * (j >> 2));
-#pragma unroll
-                for (int n = 0; n < M::VW; ++n) v[j][n] = live ? v[j][n] : 0u;
-                if constexpr (FMT == KV_U4) z[j] = live ? z[j] : 0u;
-            }
-        }
-        if (r < M::LR) {
-            uint32_t y[4];
-            if constexpr (FMT == KV_U4) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = kv_masked_record<FMT>(z[j]);
-                value_zeros(z, y);
-            }
-#pragma unroll
-            for (int e = 0; e < M::E; ++e) t[half][e * M::LR + r] = value_fragment<FMT, D>(v, y, e);
-        }
     }
 };
 
@@ -173,7 +109,7 @@ template <int FMT, int D, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     using M = ManyLayout<FMT, D>;
-    constexpr int DT = D / 32, ST = D / 16, RUNS = 8 / WAVES;
+    constexpr int DT = D / 32, ST = D / 16, PARTS = 8 / WAVES;
     __shared__ ManyLds<FMT, D> lds;
 
     const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
@@ -220,8 +156,8 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
     constexpr int FK = D == 256 ? ST : 4, FV = 4;
     half8_t fk[FK], fv[FV], p[2][2];
     float4_t kr, vr;                                   // scales of the 4 tokens that come next
-    auto key = [&](int n, int c) { return lds.k[(uint32_t)(n + 5) % lds.KRING][2 * c + g][r]; };
-    auto value = [&](int n, int j) { return lds.v[(uint32_t)(n + 5) % lds.VRING][j / DT][g][32 * (j % DT) + r]; };
+    auto key = [&](int n, int c) { return lds.k[(uint32_t)(n + 40) % lds.KRING][2 * c + g][r]; };
+    auto value = [&](int n, int j) { return lds.v[(uint32_t)(n + 40) % lds.VRING][j / DT][g][32 * (j % DT) + r]; };
     auto k_scale = [&](int n, int x) { return *reinterpret_cast<const float4_t*>(&lds.ks[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]); };
     auto v_scale = [&](int n, int x) { return *reinterpret_cast<const float4_t*>(&lds.vs[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]); };
     // The scores of an even step n, with the fragments that follow; step n - 1 weighs nothing.
@@ -247,7 +183,7 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
             o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(j < FV ? fv[j % FV] : value(n, j), p[1][j / DT], o[j % DT], 0, 0, 0);
         p[1][0] = p[1][1] = half8_t{};
     };
-    auto attend = [&](int i, auto U, bool whole, uint64_t seen) {
+    auto attend = [&](int i, auto U, bool whole, uint64_t seen, auto&& beside) {
         constexpr int u = U();
         const int n = 2 * i + u;
         float sum = 0.0f;
@@ -267,6 +203,7 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
             }
 #pragma unroll
             for (int c = x * ST / 4; c < (x + 1) * ST / 4; ++c) products(c);
+            beside(x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], nm));
@@ -320,109 +257,137 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
         l += sum;
     };
 
-    // Half of the waves carry keys (and the first of them the scales), two tiles ahead,
-    // the others values, one ahead.
-    struct Carry {
-        ManyStage<FMT, D> st[RUNS];
-        uint32_t k, v;                                 // records
-    };
-    struct Pages {
-        uint32_t own[RUNS], lane;                      // of the wave's tokens, of token `lane`
-    };
+    // Each wave carries an eighth of a tile from memory to LDS: part w is the keys of
+    // tokens 8 w .. 8 w + 7, and the values of k-slots (16 tokens w / 2, half w % 2).  Keys
+    // go two tiles ahead, values one; each is asked for a tile before it is stored.
     const ManyPages pages(a, b, h);
-    const bool keys = wave < WAVES / 2;
-    const int role = keys ? wave : wave - WAVES / 2;
+    uint32_t kc[PARTS][M::KW], kz[PARTS], vc[PARTS][8][M::VB < 4 ? 1 : M::VB / 4];
+    // Past the last tile the last one is carried again, into parts that nothing reads.
+    auto base_of = [&](int i) { return rg.tile(t0 + (i < nt ? i : nt - 1)) * kT; };
+    auto part = [&](int x) { return wave * PARTS + x; };
+    auto find = [&](int base) { return pages.page(base + lane); };                 // token `lane`'s page
+    // Bit n: token n lies in a page that exists and some row of the block sees it.
+    auto live_of = [&](int base, uint32_t page) -> uint64_t { return __ballot(pages.there(page) & rg.live(base + lane)); };
+    auto load_keys = [&](auto& c, auto& z, int base, uint32_t page) {
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) {
+            const int first = base + 8 * part(x) + (lane & 7);
+            const uint32_t own = __builtin_amdgcn_readlane(page, 8 * part(x));
+            load_bytes<M::KB>(a.c.k + (pages.at(own, first, L::ROW) + (uint32_t)((lane >> 3) * M::KB)), c[x]);
+            if constexpr (FMT == KV_U4) load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + pages.at(own, first, 4), &z[x]);
+        }
+    };
+    auto store_keys = [&](const auto& c, const auto& z, int i) {
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) {
+            auto& t = lds.k[(uint32_t)(2 * i + (part(x) >> 2) + 40) % lds.KRING];
+            const half2_t mz = FMT == KV_U4 ? minus_zero(z[x]) : half2_t{(_Float16)0.0f, (_Float16)0.0f};
+#pragma unroll
+            for (int f = 0; f < M::KF; ++f)
+                t[(lane >> 3) * M::KF + f][8 * (part(x) & 3) + (lane & 7)] = codes8<FMT>(c[x] + f * (FMT == KV_U4 ? 1 : 2), mz);
+        }
+    };
+    auto load_values = [&](auto& c, int base, uint32_t page) {
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) {
+            const int first = base + 16 * (part(x) >> 1) + 4 * (part(x) & 1);
+            const uint32_t own = __builtin_amdgcn_readlane(page, 16 * (part(x) >> 1));
+            const uint8_t* vp = a.c.v + (pages.at(own, first, L::ROW) + (uint32_t)((M::LR < 64 ? lane & (M::LR - 1) : lane) * M::VB));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) load_bytes<M::VB>(vp + ((j & 3) + 8 * (j >> 2)) * L::ROW, c[x][j]);
+        }
+    };
+    // What no row sees may hold anything: its value becomes 0.
+    auto store_values = [&](const auto& c, int i, uint64_t live) {
+#pragma unroll
+        for (int x = 0; x < PARTS; ++x) {
+            auto& t = lds.v[(uint32_t)(2 * i + (part(x) >> 2) + 40) % lds.VRING][part(x) >> 1 & 1][part(x) & 1];
+            const int first = 16 * (part(x) >> 1) + 4 * (part(x) & 1);
+            const uint32_t own = (uint32_t)(live >> first);
+            uint32_t v[8][M::VB < 4 ? 1 : M::VB / 4], z[4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t keep = 0u - (own >> ((j & 3) + 8 * (j >> 2)) & 1u);
+#pragma unroll
+                for (int n = 0; n < (M::VB < 4 ? 1 : M::VB / 4); ++n) v[j][n] = c[x][j][n] & keep;
+            }
+            if constexpr (FMT == KV_U4) {
+                const uint2 lo = *reinterpret_cast<const uint2*>(&lds.vz[i & 3][first]), hi = *reinterpret_cast<const uint2*>(&lds.vz[i & 3][first + 8]);
+                z[0] = lo.x; z[1] = lo.y; z[2] = hi.x; z[3] = hi.y;
+            }
+#pragma unroll
+            for (int e = 0; e < M::E; ++e) {
+                const half8_t y = value_fragment<FMT, D>(v, z, e);
+                if (M::LR == 64 || lane < M::LR) t[e * M::LR + lane] = y;
+            }
+        }
+    };
+    // Wave 0: the records of token `lane`, with the keys.
+    uint32_t k_rec = 0, v_rec = 0;
     float sv_ref = 0.0f, f_ref = 0x1p126f;             // value scales below sv_ref fit the reference 2^(e_put - 126) = 1 / f_ref
     uint32_t e_put = 0;
-    // Past the last tile the last one is staged again, into parts that nothing reads.
-    auto base_of = [&](int i) { return rg.tile(t0 + (i < nt ? i : nt - 1)) * kT; };
-    auto find = [&](Pages& p, int i) {
-        const int base = base_of(i);
-#pragma unroll
-        for (int n = 0; n < RUNS; ++n) p.own[n] = pages.page(base + 16 * (role * RUNS + n));
-        p.lane = pages.page(base + lane);
+    auto load_records = [&](uint32_t& kr, uint32_t& vr, int base, uint32_t page) {
+        const uint64_t at = pages.at(page, base + lane, 4);
+        load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + at, &kr);
+        load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.vs) + at, &vr);
     };
-    // Asks for tile i's part of this wave; bit n of the result: token n lies in a page that exists.
-    auto load = [&](Carry& c, const Pages& p, int i) -> uint64_t {
-        const int base = base_of(i);
-        if (keys) {
-#pragma unroll
-            for (int n = 0; n < RUNS; ++n) c.st[n].load_keys(a, pages, p.own[n], base + 16 * (role * RUNS + n), lane);
-            if (role == 0) {
-                const uint64_t at = pages.at(p.lane, base + lane, 4);
-                load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + at, &c.k);
-                load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.vs) + at, &c.v);
+    auto store_records = [&](uint32_t kr, uint32_t vr, int i, uint64_t live) {
+        vr = live >> lane & 1 ? kv_masked_record<FMT>(vr) : 0u;
+        const float sv = kv_scale<FMT>(vr);
+        if (__any(sv >= sv_ref)) {
+            uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(sv))) >> 23;
+            e = e > 252u ? 252u : e;
+            if (e > e_put || sv_ref == 0.0f) {
+                e_put = e;
+                f_ref = __uint_as_float((253u - e) << 23);
+                sv_ref = __uint_as_float((e + 1u) << 23);
             }
-        } else {
-#pragma unroll
-            for (int n = 0; n < RUNS; ++n) c.st[n].load_values(a, pages, p.own[n], base + 16 * (role * RUNS + n), lane);
         }
-        return __ballot(pages.there(p.lane));
-    };
-    auto store = [&](Carry& c, int i, uint64_t there) {
-        const int base = base_of(i);
-        const bool whole = (there == ~0ull) & rg.whole(base, kT);
-        if (!keys) {
-#pragma unroll
-            for (int n = 0; n < RUNS; ++n) {
-                const int run = role * RUNS + n;
-                c.st[n].store_values(lds.v[(uint32_t)(2 * i + (run >> 1) + 5) % lds.VRING][run & 1], rg, base + 16 * run, there >> (16 * run) & 1, whole, lane);
-            }
-            return;
-        }
-#pragma unroll
-        for (int n = 0; n < RUNS; ++n) c.st[n].store_keys(lds.k[(uint32_t)(2 * i + ((role * RUNS + n) >> 1) + 5) % lds.KRING], (role * RUNS + n) & 1, lane);
-        if (role == 0) {
-            float sv = kv_scale<FMT>(kv_masked_record<FMT>(c.v));
-            if (!whole) sv = (bool)(there >> lane & 1) & rg.live(base + lane) ? sv : 0.0f;
-            if (__any(sv >= sv_ref)) {
-                uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(sv))) >> 23;
-                e = e > 252u ? 252u : e;
-                if (e > e_put || sv_ref == 0.0f) {
-                    e_put = e;
-                    f_ref = __uint_as_float((253u - e) << 23);
-                    sv_ref = __uint_as_float((e + 1u) << 23);
-                }
-            }
-            lds.ks[i & 3][lane] = kv_scale<FMT>(c.k) * unit_s;
-            lds.vs[i & 3][lane] = sv * f_ref;
-            lds.e[i & 3] = e_put;
-        }
+        lds.ks[i & 3][lane] = kv_scale<FMT>(kr) * unit_s;
+        lds.vs[i & 3][lane] = sv * f_ref;
+        lds.e[i & 3] = e_put;
+        if constexpr (FMT == KV_U4) lds.vz[i & 3][lane] = __builtin_bit_cast(uint16_t, (_Float16)(__builtin_bit_cast(_Float16, (uint16_t)(vr >> 16)) * (_Float16)-0x1p-9f));
     };
 
-    // th0 to th2: the tokens that are there of tiles i, i + 1 and i + 2 (th2: keys only)
-    Carry st;
-    Pages pg;                                          // of the tile to load next
+    // Of tiles i to i + 3: first position, pages (from i + 2) and live tokens (to i + 2).
+    int b0 = base_of(0), b1 = base_of(1), b2 = base_of(2), b3 = base_of(3);
+    uint32_t pg2 = 0, pg3 = 0;
     uint64_t th0 = 0, th1 = 0, th2 = 0;
     {
         // the first tiles' pages, codes and queries are all asked for before any is waited for
-        Carry st0, st1;
-        Pages p0, p1;
+        uint32_t k0[PARTS][M::KW], k1[PARTS][M::KW], z0[PARTS], z1[PARTS], v0[PARTS][8][M::VB < 4 ? 1 : M::VB / 4], r0k = 0, r0v = 0, r1k = 0, r1v = 0;
+        const uint32_t p0 = nt > 0 ? find(b0) : 0, p1 = nt > 0 ? find(b1) : 0;
+        if (nt > 0) pg2 = find(b2);
+        load_queries<D>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, qf);
         if (nt > 0) {
-            find(p0, 0);
-            find(p1, 1);
-            find(pg, 2);
-        }
-        load_queries<FMT, D>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, qf);
-        if (nt > 0) {
-            th0 = load(st0, p0, 0);
-            if (keys) {
-                th1 = load(st1, p1, 1);
-                th2 = load(st, pg, 2);
-            } else {
-                th1 = load(st, p1, 1);
+            load_keys(k0, z0, b0, p0);
+            load_values(v0, b0, p0);
+            load_keys(k1, z1, b1, p1);
+            load_values(vc, b1, p1);
+            load_keys(kc, kz, b2, pg2);
+            if (wave == 0) {
+                load_records(r0k, r0v, b0, p0);
+                load_records(r1k, r1v, b1, p1);
+                load_records(k_rec, v_rec, b2, pg2);
             }
+            th0 = live_of(b0, p0);
+            th1 = live_of(b1, p1);
+            th2 = live_of(b2, pg2);
+            pg3 = find(b3);
         }
         // the step before the first: no weight, but products with its values are taken
-        half8_t* before = &lds.v[4][0][0][0];
+        half8_t* before = &lds.v[39 % lds.VRING][0][0][0];
         for (int x = threadIdx.x; x < 4 * D; x += WAVES * 64) before[x] = half8_t{};
         unit_s = scale_queries<FMT, D, WAVES>(a, wave, lds.top, qf);
         if (nt > 0) {
-            store(st0, 0, th0);
-            if (keys) {
-                store(st1, 1, th1);
-                find(pg, 3);
+            if (wave == 0) {
+                store_records(r0k, r0v, 0, th0);
+                store_records(r1k, r1v, 1, th1);
             }
+            store_keys(k0, z0, 0);
+            store_keys(k1, z1, 1);
+            if constexpr (FMT == KV_U4) __syncthreads();         // its values' zero-points come from the records
+            store_values(v0, 0, th0);
         }
     }
     __syncthreads();
@@ -430,31 +395,46 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
     if (nt > 0) e_ref = __builtin_amdgcn_readfirstlane(lds.e[0]);
     __syncthreads();
     for (int i = 0; i < nt; ++i) {
-        // Into what the last tile left: keys of tile i + 2, values of tile i + 1.  The two
-        // waves of a SIMD do so at different times, the one beside the other's products.
-        uint64_t next = 0;
-        if (keys) {
-            store(st, i + 2, th2);
-            next = load(st, pg, i + 3);
-            find(pg, i + 4);
+        // Into what the last tile left, beside the products: keys and records of tile i + 2,
+        // values of tile i + 1.
+        auto carry_keys = [&](int x) {
+            if (x == 0) store_keys(kc, kz, i + 2);
+            if (x == 1) load_keys(kc, kz, b3, pg3);
+        };
+        auto carry_values = [&](int x) {
+            if (x == 0) store_values(vc, i + 1, th1);
+            if (x == 2) load_values(vc, b2, pg2);
+        };
+        if (wave == 0) {
+            store_records(k_rec, v_rec, i + 2, th2);
+            load_records(k_rec, v_rec, b3, pg3);
         }
+        const uint64_t th3 = live_of(b3, pg3);
         // a tile that none of the wave's rows sees takes part with no weight
-        const int base = base_of(i);
+        const int base = b0;
         const bool whole = (th0 == ~0ull) & wr.whole(base, kT);
         uint64_t seen = ~0ull;
         const uint32_t e = lds.e[(i + 1) & 3];
         if (!whole) seen = seen_bits(a, q, qi, base, th0);
-        if (has_rows) attend(i, std::integral_constant<int, 0>{}, whole, seen);
-        if (!keys) {
-            store(st, i + 1, th1);
-            next = load(st, pg, i + 2);
-            find(pg, i + 3);
+        if (has_rows) {
+            attend(i, std::integral_constant<int, 0>{}, whole, seen, carry_keys);
+            e_next = __builtin_amdgcn_readfirstlane(e);
+            attend(i, std::integral_constant<int, 1>{}, whole, seen, carry_values);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) carry_keys(x);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) carry_values(x);
         }
-        e_next = __builtin_amdgcn_readfirstlane(e);
-        if (has_rows) attend(i, std::integral_constant<int, 1>{}, whole, seen);
+        b0 = b1;
+        b1 = b2;
+        b2 = b3;
+        b3 = base_of(i + 4);
+        pg2 = pg3;
+        pg3 = find(b3);
         th0 = th1;
-        th1 = keys ? th2 : next;
-        th2 = next;
+        th1 = th2;
+        th2 = th3;
         __syncthreads();
     }
 
@@ -463,23 +443,25 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
     if (!ok) return;
     const float y0 = l == 0.0f ? 0.0f : __uint_as_float((e_ref + 1u) << 23) * L::UNIT / l;
     const float ls = l == 0.0f ? -__builtin_inff() : __builtin_log2f(l) - nm;
-    constexpr int HI = 32 / M::LR, RUN = 4 * M::E;          // accumulator row m is lane m % LR, element HI d + m / LR
+    constexpr int HB = M::LR / 32, RUN = 4 * M::E;          // accumulator row m of O[e HB + x] is element e of lane 32 x + m
 #pragma unroll
-    for (int n = 0; n < 4 / HI; ++n) {
-        float y[RUN];
+    for (int x = 0; x < HB; ++x)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int n = 0; n < 4; ++n) {
+            float y[RUN];
 #pragma unroll
-            for (int e = 0; e < M::E; ++e) y[j * M::E + e] = l == 0.0f ? 0.0f : o[e / HI][4 * (e % HI * 2 + n) + j] * y0;
-        const int64_t d = to * D + (8 * n + 4 * g) * M::E;
-        if (sp.splits > 1) {
-            float* p = po + (int64_t)split * a.tokens * a.q_heads * D + d;
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < RUN; e += 4) *reinterpret_cast<float4_t*>(p + e) = float4_t{y[e], y[e + 1], y[e + 2], y[e + 3]};
-        } else {
-            store_out<RUN>(a, d, y);
+                for (int e = 0; e < M::E; ++e) y[j * M::E + e] = l == 0.0f ? 0.0f : o[e * HB + x][4 * n + j] * y0;
+            const int64_t d = to * D + (32 * x + 8 * n + 4 * g) * M::E;
+            if (sp.splits > 1) {
+                float* p = po + (int64_t)split * a.tokens * a.q_heads * D + d;
+#pragma unroll
+                for (int e = 0; e < RUN; e += 4) *reinterpret_cast<float4_t*>(p + e) = float4_t{y[e], y[e + 1], y[e + 2], y[e + 3]};
+            } else {
+                store_out<RUN>(a, d, y);
+            }
         }
-    }
     if (g == 0) {
         if (sp.splits > 1) pl[(int64_t)split * a.tokens * a.q_heads + to] = ls;
         else if (a.lse) a.lse[to] = ls * 0x1.62e43p-1f;
