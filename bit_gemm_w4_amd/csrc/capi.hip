@@ -635,8 +635,9 @@ bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool poin
     if (p->q_heads < a->c.heads || p->q_heads > 16384 || p->q_heads % a->c.heads)
         return fail_in(fn, BG_ERR_SHAPE, "q_heads=%lld is not a multiple of kv_heads=%lld", p->q_heads, a->c.heads);
     if (p->max_pages < 1 || p->max_pages > INT32_MAX) return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld out of range", p->max_pages);
-    if (p->max_pages > (INT32_MAX >> a->c.page_shift))
-        return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld pages of %lld tokens pass 2^31 positions", p->max_pages, p->cache->page_size);
+    // positions less a window and a call's queries have to fit 32 bits
+    if (p->max_pages > ((INT32_MAX - 2 * kMaxTokens) >> a->c.page_shift))
+        return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld pages of %lld tokens pass 2^31 - 2^25 positions", p->max_pages, p->cache->page_size);
     if (p->max_q < 1 || p->max_q > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "max_q=%lld out of range", p->max_q);
     if (p->max_kv < 0) return fail_in(fn, BG_ERR_SHAPE, "max_kv=%lld is negative", p->max_kv);
     if (p->window < 0 || p->sinks < 0) return fail_in(fn, BG_ERR_SHAPE, "window=%lld and sinks=%lld must not be negative", p->window, p->sinks);
@@ -671,7 +672,7 @@ bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool poin
     a->max_q = p->max_q < p->tokens ? p->max_q : p->tokens;
     const int64_t room = p->max_pages << a->c.page_shift;
     a->max_kv = p->max_kv == 0 || p->max_kv > room ? room : p->max_kv;
-    a->window = p->window > INT32_MAX ? 0 : p->window;   // positions stay below 2^31
+    a->window = p->window >= room ? 0 : p->window;      // such a window holds every position
     a->sinks = a->window ? (p->sinks > INT32_MAX ? INT32_MAX : p->sinks) : 0;
     a->tree = tree ? p->tree : nullptr;
     a->tree_words = tree ? p->tree_words : 0;

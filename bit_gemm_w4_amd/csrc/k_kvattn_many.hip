@@ -100,7 +100,7 @@ __device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& 
     } else {
         const int at = q.first + i;
         m = low_bits(at + 1 - base);
-        if (a.window) m &= ~low_bits(at - (int)a.window + 1 - base) | low_bits((int)a.sinks - base);
+        if (a.window) m &= ~low_bits(at - base - (int)a.window + 1) | low_bits((int)a.sinks - base);
     }
     return m & there;
 }

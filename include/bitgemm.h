@@ -558,7 +558,7 @@ bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t 
  *              later queries are left alone)
  *   max_kv     at least every kv_lens entry, or 0 for the block table's width:
  *              sizes the split over positions; a smaller value costs only speed
- *   kv_lens    clamped to 0 .. max_pages * page_size
+ *   kv_lens    clamped to 0 .. max_pages * page_size, which is at most 2^31 - 2^25
  *   out        [tokens][q_heads][head_dim] of dtype (F16 or BF16)
  *   lse        [tokens][q_heads] binary32: ln of the sum of exp(scale * score),
  *              or NULL

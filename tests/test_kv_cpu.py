@@ -205,6 +205,15 @@ def test_tokens_times_heads_are_bounded(L):
     assert L.kv_attn(ctypes.addressof(a), P, 1 << 40, None) == E_SHAPE
 
 
+def test_positions_leave_room_for_a_window_in_32_bits(L):
+    for shift in (4, 6, 10):
+        c = cache(page_size=1 << shift)
+        most = (2 ** 31 - 1 - 2 ** 25) >> shift
+        for pages, status in ((most, E_WS), (most + 1, E_SHAPE)):       # E_WS: past the sizes' checks
+            a = attn(c, tokens=1, batch=1, max_q=1, cu_q=None, max_pages=pages)
+            assert L.kv_attn(ctypes.addressof(a), None, 0, None) == status
+
+
 def test_workspace_follows_the_split(L):
     """Many rows of a short sequence, or more blocks than the device holds at once, need none; it grows with neither pages nor window alone."""
     c = cache(pages=100000, kv_heads=8)
