@@ -8,7 +8,7 @@
 //
 // Bound by HBM: a cache token is 2 D codes and 8 bytes of records per kv
 // head.  A wave takes 32 tokens at a time straight from memory into registers
-// (no LDS, no barrier in the loop), with the next 32 in flight:
+// (no LDS, no barrier in the loop), with the next 32 in flight where registers allow:
 //   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' codes, B = 16 rows
 //   O^T += V^T P^T  the same instruction, A = 16 head elements of 32 tokens
 // The tile's pages are looked up two tiles ahead; 8 waves a CU with two tiles each
@@ -79,7 +79,7 @@ struct Tile {
 
 // RT row tiles of 16 rows per wave.
 template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 2 : 1) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+__global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     constexpr int DT = D / 16, ST = D / 32, PAD = D + 4;
     __shared__ float o_lds[kWaves][16][PAD];
@@ -247,19 +247,34 @@ __global__ void __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 2 : 1) k_kv
         }
     };
 
-    Tile<FMT, D> ta, tb;
-    if (i < t1) {
-        ta.load(a, pa, h, rg.tile(i), r, g);
-        find(pa, i + 2 * kWaves);
-    }
-    for (; i < t1; i += 2 * kWaves) {
-        if (i + kWaves < t1) tb.load(a, pb, h, rg.tile(i + kWaves), r, g);
-        find(pb, i + 3 * kWaves);
-        compute(ta, rg.tile(i));
-        if (i + kWaves >= t1) break;
-        if (i + 2 * kWaves < t1) ta.load(a, pa, h, rg.tile(i + 2 * kWaves), r, g);
-        find(pa, i + 4 * kWaves);
-        compute(tb, rg.tile(i + kWaves));
+    if constexpr (RT * D > 128) {
+        // One tile at a time leaves registers for two waves a SIMD, which cover each other's
+        // waits: 64 rows of 16 x 8192 tokens, E4M3, D = 128, 92 us with two tiles and one wave,
+        // 77 so; 48 rows of 64 x 2000, INT8, 114 and 78; 18 x 2 queries of 4668, 4 bits,
+        // D = 256, 59 and 46.
+        Tile<FMT, D> t;
+        for (; i < t1; i += kWaves) {
+            t.load(a, pa, h, rg.tile(i), r, g);
+            pa[0] = pb[0];
+            pa[1] = pb[1];
+            find(pb, i + 2 * kWaves);
+            compute(t, rg.tile(i));
+        }
+    } else {
+        Tile<FMT, D> ta, tb;
+        if (i < t1) {
+            ta.load(a, pa, h, rg.tile(i), r, g);
+            find(pa, i + 2 * kWaves);
+        }
+        for (; i < t1; i += 2 * kWaves) {
+            if (i + kWaves < t1) tb.load(a, pb, h, rg.tile(i + kWaves), r, g);
+            find(pb, i + 3 * kWaves);
+            compute(ta, rg.tile(i));
+            if (i + kWaves >= t1) break;
+            if (i + 2 * kWaves < t1) ta.load(a, pa, h, rg.tile(i + 2 * kWaves), r, g);
+            find(pa, i + 4 * kWaves);
+            compute(tb, rg.tile(i + kWaves));
+        }
     }
 
     // join the waves, 16 rows at a time
@@ -385,22 +400,29 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
     if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
 }
 
-// Rows of a block, and how positions are split over blocks.
+// The kernel, rows of a block, and how positions are split over blocks.
 struct Plan {
     bool many;
     int rt;
     unsigned row_blocks;
     KvSplit sp;
+    double us;
 };
 
-Plan plan_of(const KvAttnArgs& a) {
+// The plan with one of the kernels that takes the least time by this model: rounds of the
+// blocks that the device holds at once, each a start and its tiles; the join; and the
+// partials' way to memory and back at 4 TB/s.  Many rows: one block a CU, a start worth 3
+// tiles.  Few: two blocks a CU, each wave a quarter of the tiles, a start worth 2 of its.
+// As many splits as fill the device, for which this stands, ran 136 blocks of 16 tiles as
+// two rounds of 8 tiles in 94 us (one of 16: 58), and 35 sequences of 11687 tokens,
+// D = 256, in 64 (47).
+Plan plan_with(const KvAttnArgs& a, bool many) {
     Plan p;
     const int64_t rows = a.max_q * (a.q_heads / a.c.heads);
-    // Up to 96 rows the few-row kernel is ahead (64 rows of 16 x 8192 tokens, E4M3: 116
-    // against 131 us; 128 rows: 173 against 138).
-    p.many = rows > 96;
-    p.rt = rows <= 16 || a.c.dim == 256 ? 1 : 2;
-    const int per_block = p.many ? (a.c.dim == 256 ? 128 : 256) : 16 * p.rt, tile = p.many ? 64 : 32;
+    const bool wide = a.c.dim == 256, narrow = a.c.dim == 64;
+    p.many = many;
+    p.rt = rows <= 16 || wide ? 1 : 2;
+    const int per_block = many ? (wide ? 128 : 256) : 16 * p.rt, tile = many ? 64 : 32;
     p.row_blocks = (unsigned)((rows + per_block - 1) / per_block);
     // positions a row block can see, in tiles
     int64_t seen = a.max_kv;
@@ -409,23 +431,16 @@ Plan plan_of(const KvAttnArgs& a) {
         seen = most < seen ? most : seen;
     }
     const int64_t tiles = (seen + tile - 1) / tile > 0 ? (seen + tile - 1) / tile : 1;
-    // The number of splits that takes the least time by this model: rounds of the blocks
-    // that the device holds at once, each a start and its tiles; the join; and the
-    // partials' way to memory and back at 4 TB/s.  Many rows: one block a CU, a tile
-    // 2.1 us, a start worth 3.  Few: two blocks a CU (one where registers fill it), each
-    // wave a quarter of the tiles, 2 us each, a start worth 2.  As many splits as fill the
-    // device, for which this stands, ran 136 blocks of 16 tiles as two rounds of 8 tiles in
-    // 94 us (one of 16: 58), and 35 sequences of 11687 tokens, D = 256, in 64 (47).
-    const int64_t blocks = a.batch * a.c.heads * p.row_blocks;
-    const int64_t room = p.many || a.c.dim == 256 || (p.rt == 2 && a.c.dim == 128) ? 256 : 512;
-    const double partials = (double)(a.tokens * a.q_heads * a.c.dim) * 8.0 / 4.0e6 / 2.0;
+    const int64_t blocks = a.batch * a.c.heads * p.row_blocks, room = many ? 256 : 512;
+    const double tile_us = many ? (wide ? 3.5 : narrow ? 1.65 : 2.1) : (wide ? 3.0 : 2.1);      // measured, device full
+    const double partials = (double)(a.tokens * a.q_heads * a.c.dim) * 8.0 / 4.0e6;
     int64_t splits = 1;
-    double best = 1e30;
+    p.us = 1e30;
     for (int64_t s = 1; s <= 256 && s <= tiles; ++s) {
-        const double run = (double)((tiles + s - 1) / s), rounds = (double)((blocks * s + room - 1) / room);
-        const double cost = rounds * (p.many ? 3.0 + run : 2.0 + (double)(((int64_t)run + 3) / 4)) + (s == 1 ? 0.0 : (p.many ? 2.0 : 1.5) + s * (partials + 1.0 / 64.0));
-        if (cost < best) {
-            best = cost;
+        const int64_t run = (tiles + s - 1) / s, rounds = (blocks * s + room - 1) / room;
+        const double us = (double)(rounds * (many ? 3 + run : 2 + (run + 3) / 4)) * tile_us + (s == 1 ? 0.0 : (many ? 4.0 : 3.0) + (double)s * (partials + 0.03));
+        if (us < p.us) {
+            p.us = us;
             splits = s;
         }
         if (blocks * s > 4 * room) break;
@@ -433,6 +448,17 @@ Plan plan_of(const KvAttnArgs& a) {
     p.sp.tiles = (int)((tiles + splits - 1) / splits);
     p.sp.splits = (int)((tiles + p.sp.tiles - 1) / p.sp.tiles);
     return p;
+}
+
+// Up to 32 rows (16 at D = 256: one block's) the few-row kernel reads each code once; from
+// there on by the model.  16 x 8192 tokens, E4M3, D = 128: 96 rows 104 us with few, 119 with
+// many; 192 rows 151 and 146; 65536 tokens in 4 bits, 192 rows: 116 and 94; 1000 tokens,
+// INT8, 192 rows: 19 and 27; 4 x 8192, INT8, D = 256, 128 rows: 98 and 75.
+Plan plan_of(const KvAttnArgs& a) {
+    const Plan few = plan_with(a, false);
+    if (a.max_q * (a.q_heads / a.c.heads) <= (a.c.dim == 256 ? 16 : 32)) return few;
+    const Plan many = plan_with(a, true);
+    return many.us < few.us ? many : few;
 }
 
 }  // namespace
