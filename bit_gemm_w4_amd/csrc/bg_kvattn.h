@@ -375,7 +375,7 @@ void for_format(int fmt, int dim, F&& f) {
     else on_dim(std::integral_constant<int, KV_U4>{});
 }
 
-// Many query rows per kv head, rows of row_blocks blocks (k_kvattn_many.hip).
-const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, float* po, float* pl, hipStream_t s);
+// Many query rows per kv head, rows of row_blocks blocks of 8 waves (4 at D = 256; either at D = 64) (k_kvattn_many.hip).
+const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s);
 
 }  // namespace bg

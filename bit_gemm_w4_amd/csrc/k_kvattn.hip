@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
 
 // The kernel, rows of a block, and how positions are split over blocks.
 struct Plan {
-    bool many;
+    int waves;                            // of a block of the many-row kernel; 0: the few-row kernel
     int rt;
     unsigned row_blocks;
     KvSplit sp;
@@ -411,18 +411,18 @@ struct Plan {
 
 // The plan with one of the kernels that takes the least time by this model: rounds of the
 // blocks that the device holds at once, each a start and its tiles; the join; and the
-// partials' way to memory and back at 4 TB/s.  Many rows: one block a CU, a start worth 3
-// tiles.  Few: two blocks a CU, each wave a quarter of the tiles, a start worth 2 of its.
+// partials' way to memory and back at 4 TB/s.  Many rows: one block a CU (two of four
+// waves at D = 64), a start worth 3 tiles.  Few: two blocks a CU, each wave a quarter of the tiles, a start worth 2 of its.
 // As many splits as fill the device, for which this stands, ran 136 blocks of 16 tiles as
 // two rounds of 8 tiles in 94 us (one of 16: 58), and 35 sequences of 11687 tokens,
 // D = 256, in 64 (47).
-Plan plan_with(const KvAttnArgs& a, bool many) {
+Plan plan_with(const KvAttnArgs& a, int waves) {
     Plan p;
     const int64_t rows = a.max_q * (a.q_heads / a.c.heads);
-    const bool wide = a.c.dim == 256, narrow = a.c.dim == 64;
-    p.many = many;
+    const bool many = waves > 0, wide = a.c.dim == 256, narrow = a.c.dim == 64;
+    p.waves = waves;
     p.rt = rows <= 16 || wide ? 1 : 2;
-    const int per_block = many ? (wide ? 128 : 256) : 16 * p.rt, tile = many ? 64 : 32;
+    const int per_block = many ? 32 * waves : 16 * p.rt, tile = many ? 64 : 32;
     p.row_blocks = (unsigned)((rows + per_block - 1) / per_block);
     // positions a row block can see, in tiles
     int64_t seen = a.max_kv;
@@ -431,8 +431,8 @@ Plan plan_with(const KvAttnArgs& a, bool many) {
         seen = most < seen ? most : seen;
     }
     const int64_t tiles = (seen + tile - 1) / tile > 0 ? (seen + tile - 1) / tile : 1;
-    const int64_t blocks = a.batch * a.c.heads * p.row_blocks, room = many ? 256 : 512;
-    const double tile_us = many ? (wide ? 3.5 : narrow ? 1.65 : 2.1) : (wide ? 3.0 : 2.1);      // measured, device full
+    const int64_t blocks = a.batch * a.c.heads * p.row_blocks, room = many && (waves == 8 || wide) ? 256 : 512;
+    const double tile_us = many ? (wide ? 3.5 : !narrow ? 2.1 : waves == 8 ? 1.65 : 1.85) : (wide ? 3.0 : 2.1);      // measured, device full
     const double partials = (double)(a.tokens * a.q_heads * a.c.dim) * 8.0 / 4.0e6;
     int64_t splits = 1;
     p.us = 1e30;
@@ -453,12 +453,18 @@ Plan plan_with(const KvAttnArgs& a, bool many) {
 // Up to 32 rows (16 at D = 256: one block's) the few-row kernel reads each code once; from
 // there on by the model.  16 x 8192 tokens, E4M3, D = 128: 96 rows 104 us with few, 119 with
 // many; 192 rows 151 and 146; 65536 tokens in 4 bits, 192 rows: 116 and 94; 1000 tokens,
-// INT8, 192 rows: 19 and 27; 4 x 8192, INT8, D = 256, 128 rows: 98 and 75.
+// INT8, 192 rows: 19 and 27; 4 x 8192, INT8, D = 256, 128 rows: 98 and 75.  D = 64, blocks of
+// eight waves and of four: 112 rows of 12 x 26287 tokens in 4 bits 238 and 189 us, 800 of
+// 9 x 6000, E4M3, 69 and 62; 256 of 16 x 8192 122 and 136, 8192 of 2 x 4096 190 and 202.
 Plan plan_of(const KvAttnArgs& a) {
-    const Plan few = plan_with(a, false);
-    if (a.max_q * (a.q_heads / a.c.heads) <= (a.c.dim == 256 ? 16 : 32)) return few;
-    const Plan many = plan_with(a, true);
-    return many.us < few.us ? many : few;
+    Plan best = plan_with(a, 0);
+    if (a.max_q * (a.q_heads / a.c.heads) <= (a.c.dim == 256 ? 16 : 32)) return best;
+    for (int waves : {8, 4}) {
+        if (a.c.dim != 64 && waves != (a.c.dim == 256 ? 4 : 8)) continue;
+        const Plan p = plan_with(a, waves);
+        if (p.us < best.us) best = p;
+    }
+    return best;
 }
 
 }  // namespace
@@ -474,7 +480,7 @@ const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
     float* pl = po + (int64_t)p.sp.splits * a.tokens * a.q_heads * a.c.dim;
     const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, (unsigned)a.batch);
     const char* name = nullptr;
-    if (p.many) name = launch_kv_attn_many(a, p.sp, p.row_blocks, po, pl, s);
+    if (p.waves) name = launch_kv_attn_many(a, p.sp, p.row_blocks, p.waves, po, pl, s);
     else for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
         if (p.rt == 1) k_kv_attn_few<FMT(), D(), 1><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
         else if constexpr (D() != 256) k_kv_attn_few<FMT(), D(), 2><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);

@@ -2,7 +2,8 @@
 // query rows per kv head (prompt chunks, large draft trees).
 //
 // A block of eight waves takes 256 rows of one sequence and kv head, 32 to a wave
-// (head size 256: four waves, 128 rows), and walks the positions some row sees
+// (head size 256: four waves, 128 rows; head size 64: that or two blocks of four
+// waves a CU, where 256 rows would leave most of a block empty), and walks the positions some row sees
 // in tiles of 64.  With this many rows per cache byte the matrix cores bound it:
 //   S^T = K Q^T     v_mfma_f32_32x32x16_f16, A = 32 tokens, B = 32 rows
 //   O^T += V^T P^T  A = 32 head elements of 16 tokens, B = the weights in place
@@ -14,14 +15,14 @@
 // What else there is to do runs beside the products:
 // * A tile's codes turn to FP16 once per block, in LDS, as the fragments that the
 //   waves' products take (16 bytes per lane, contiguous over lanes: no bank
-//   conflicts in either direction).  Each wave carries an eighth of a tile, keys two
-//   tiles ahead and values one, between its products; one barrier a tile.
+//   conflicts in either direction).  Each wave carries an eighth of a tile (a quarter
+//   in blocks of four), keys two tiles ahead and values one, between its products; one barrier a tile.
 // * The products of the next step's scores and of the last step's values alternate
 //   (two chains that do not wait for one another), with this step's weights in the
 //   vector units' slots between them.
 // A tile of 64 positions takes a block 2.1 us (4,200 cycles, 2,048 of them in each SIMD's
 // matrix core); a block's start (pages, first codes, queries) 6 us.  2,048 queries
-// over a window of 4,096 in E4M3 (8 kv heads of 4, D = 128): 171 us, 806 TFLOP/s; the
+// over a window of 4,096 in E4M3 (8 kv heads of 4, D = 128): 165 us, 835 TFLOP/s; the
 // few-row kernel takes 460 us, a library product of 8192^3 in FP16 runs at 1,064
 // TFLOP/s.  In 16x16x32, a barrier and codes of a tile at a time: 245 us; with half of
 // the waves carrying keys and half values outside the products: 175 us.
@@ -106,7 +107,7 @@ __device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& 
 }
 
 template <int FMT, int D, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     using M = ManyLayout<FMT, D>;
     constexpr int DT = D / 32, ST = D / 16, PARTS = 8 / WAVES;
@@ -470,13 +471,17 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4) k_kv_attn_many(KvAttnAr
 
 }  // namespace
 
-const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, float* po, float* pl, hipStream_t s) {
+const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s) {
     const dim3 grid((unsigned)a.c.heads * row_blocks, (unsigned)sp.splits, (unsigned)a.batch);
     for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
-        constexpr int W = D() == 256 ? 4 : 8;
-        k_kv_attn_many<FMT(), D(), W><<<grid, W * 64, 0, s>>>(a, sp, po, pl);
+        if constexpr (D() != 256) {
+            if (waves == 8) k_kv_attn_many<FMT(), D(), 8><<<grid, 8 * 64, 0, s>>>(a, sp, po, pl);
+        }
+        if constexpr (D() != 128) {
+            if (waves == 4) k_kv_attn_many<FMT(), D(), 4><<<grid, 4 * 64, 0, s>>>(a, sp, po, pl);
+        }
     });
-    return kname("k_kv_attn_many", a.c.fmt, a.c.dim, a.c.dim == 256 ? 4 : 8);
+    return kname("k_kv_attn_many", a.c.fmt, a.c.dim, waves);
 }
 
 }  // namespace bg

@@ -139,3 +139,18 @@ def test_value_scales_that_grow_along_the_sequence(ops, fmt):  # noqa: F811
 
 def test_queries_of_very_different_size_in_one_block(ops):  # noqa: F811
     edges.test_queries_of_very_different_size_in_one_block(ops)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_lens,kv_lens,group,window,sinks,tree", [([100, 67], [100, 1000], 1, 0, 0, False), ([18], [333], 7, 0, 0, False),
+                                                                    ([25, 20], [700, 20], 5, 70, 9, False), ([64, 33], [300, 33], 2, 0, 0, True),
+                                                                    ([128, 0], [40, 50], 1, 0, 0, False)])
+def test_blocks_of_128_rows(ops, fmt, q_lens, kv_lens, group, window, sinks, tree, monkeypatch):  # noqa: F811
+    """Head size 64, up to 128 rows: two blocks of four waves a compute unit."""
+    monkeypatch.setattr(Copies, "blocks", 512)
+    c = Copies(ops, fmt, "bf16", 1, group, 64, 16, q_lens, kv_lens, seed=40, window=window, sinks=sinks, tree=tree, gone=0.1)
+    lse = torch.empty(sum(q_lens), group, device="cuda")
+    got = c.run(ops, lse=lse)
+    assert ops.last_kernel() == f"k_kv_attn_many<{fmt}, 64, 4>"
+    c.check(got, lse)
+    assert torch.equal(got, c.run(ops))
