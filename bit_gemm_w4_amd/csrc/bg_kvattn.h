@@ -133,6 +133,40 @@ __device__ __forceinline__ uint32_t kv_masked_record(uint32_t record) {
     return record;
 }
 
+// A row's references.  Its weights are over 2^m: w = 2^(score - m); its weights times their
+// value scales, which the second product takes in FP16, over 2^n, n = m + log2(1 / fb):
+// w s fb.  Both are powers of two, so that moving one is exact, and follow what the row
+// itself sees and nothing else: n the largest w |s|, which lies in 2^(T - 1) .. 2^T when
+// found and stays below FP16's 2^16; m is n (fb = 1), but for value scales so large or
+// small that the weights would leave binary32: within 2^40 of the largest weight.  With
+// one reference of the weights and one of the scales instead, a first token with 90 %
+// of the weight and a value near zero left the others' weights below FP16's range: 20 %
+// off and more at 40,000 tokens in a block.
+constexpr float kNoRef = -0x1.fffffep127f;         // of a row that has seen nothing
+constexpr float kMaxWeight = 0x1p50f;
+
+// log2 of a scale's magnitude (infinities and NaN aside); those below binary32's normal range count as its least.
+__device__ __forceinline__ float scale_log2(float s) { return __builtin_fmaxf(__builtin_amdgcn_logf(__builtin_fabsf(s)), -126.0f); }
+
+struct RowStep {
+    float l, o;                // what the move makes of the sum and of the outputs
+};
+
+// Moves a row's references: ty is the largest score so far, tp the largest score + log2
+// |value scale| of the tile, -infinity if there are none.
+template <int T>
+__device__ __forceinline__ RowStep raise_row(float& m, float& fb, float ty, float tp) {
+    const float n = m + (float)(127 - (int)(__float_as_uint(fb) >> 23));
+    const float n1 = tp > n + (T + 1) ? __builtin_ceilf(tp) - T : n;
+    const float y = __builtin_fmaxf(__builtin_ceilf(ty), kNoRef);
+    const float m1 = __builtin_fminf(__builtin_fmaxf(n1, y - 40.0f), y + 40.0f);
+    const float b = __builtin_fminf(__builtin_fmaxf(n1 - m1, -120.0f), 100.0f);
+    const RowStep f{__builtin_amdgcn_exp2f(m - m1), __builtin_amdgcn_exp2f(n - (m1 + b))};
+    m = m1;
+    fb = __uint_as_float((uint32_t)(127 - (int)b) << 23);
+    return f;
+}
+
 // Two small unsigned integers in the halves of w, read as FP16 subnormals
 // n 2^-24, to n * mul 2^-24 + add: exact.
 __device__ __forceinline__ half2_t small_pair(uint32_t w, _Float16 mul, half2_t add) {

@@ -28,11 +28,14 @@
 // Numerics.  Codes are exact in FP16 (INT8 and 4-bit codes less their offset,
 // E4M3 values); queries too, each row scaled by a power of two so BF16's range
 // fits (elements below 2^-38 of their row's largest lose bits).  Scales stay in
-// binary32: the key's on the score, the value's on the weight.  The weight times
-// the value's scale, relative to the largest so far of each, is what is rounded
-// to FP16 for the second product: off by 2^-11 at most, against 2^-8 for BF16.  The
-// reference maximum of a row moves only when a score passes it by 2^8 (weights
-// reach 256 at most), so in the steady state a tile needs no lane exchange.
+// binary32: the key's on the score, the value's on the weight.  The weight w times
+// the value's scale s is what is rounded to FP16 for the second product: off by
+// 2^-11 at most, against 2^-8 for BF16, or, where w s lies more than 2^20 below the
+// largest that the row has seen, by 2^-31 of that largest (raise_row in bg_kvattn.h).
+// A row's references follow what it sees itself: taken over all rows of a wave, a
+// value that one row sees took the others' weights out of FP16's range (at 2^24 times
+// their scale all of it).  They move only when a w s passes them by 2^8, so in the
+// steady state a tile needs no lane exchange.
 #include "bg_device.h"
 #include "bg_internal.h"
 #include "bg_kvattn.h"
@@ -121,7 +124,8 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     }
 
     half8_t qf[RT][ST];
-    float rq[RT], m[RT], l[RT];
+    // of each row: weights are over 2^m, weights times value scales over 2^m / fb
+    float rq[RT], m[RT], l[RT], fb[RT];
     int qi[RT];
     float4_t o[RT][DT];
 #pragma unroll
@@ -131,14 +135,12 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         qi[x] = (ok ? row : rows - 1) / G;
         const int64_t at = (q.q0 + qi[x]) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs;
         rq[x] = load_query<FMT, D, 4>(a, at, g, ok, qf[x]);
-        m[x] = -__builtin_inff();
+        m[x] = kNoRef;
         l[x] = 0.0f;
+        fb[x] = 1.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[x][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    uint32_t e_ref = 0;                   // biased exponent that the weights' value scales are relative to
-    float sv_ref = 0.0f;                  // scales below this fit it
-    float f_ref = 0x1p126f;               // 2^(126 - e_ref)
 
     auto compute = [&](Tile<FMT, D>& t, int tile) {
         const int base = tile * 32;
@@ -153,33 +155,6 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
 #pragma unroll
                 for (int w = 0; w < L::VW; ++w) t.v[j][w] = live ? t.v[j][w] : 0u;
             }
-        }
-        float sv[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sv[j] = kv_scale<FMT>(t.vs[j]);
-        // value scales: the reference exponent follows the largest
-        {
-            float top = sv[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, sv[j]);
-            if (__any(top >= sv_ref)) {
-                top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top)) >> 23;
-                e = e > 252u ? 252u : e;
-                if (e > e_ref || sv_ref == 0.0f) {
-                    const float f = e - e_ref > 126u ? 0.0f : __uint_as_float((127u - (e - e_ref)) << 23);
-#pragma unroll
-                    for (int x = 0; x < RT; ++x)
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) o[x][d] *= f;
-                    e_ref = e;
-                    f_ref = __uint_as_float((253u - e) << 23);
-                    sv_ref = __uint_as_float((e + 1u) << 23);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sv[j] *= f_ref;
         }
         // scores
         float4_t s[RT][2];
@@ -197,44 +172,57 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         half8_t p[RT];
 #pragma unroll
         for (int x = 0; x < RT; ++x) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = s[x][j >> 2][j & 3] * kv_scale<FMT>(t.ks[j]);
-            if (!whole) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int at = first_token + (j & 3) + 16 * (j >> 2);
-                    y[j] = (t.there >> (j >> 2) & 1) && kv_sees(a, q, qi[x], at) ? y[j] : -__builtin_inff();
-                }
-            }
-            float top = y[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, y[j]);
-            if (__any(top * rq[x] > m[x] + 8.0f)) {
-                top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-                const float mn = __builtin_fmaxf(m[x], top * rq[x]);
-                const float f = mn == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[x] - mn);
-                m[x] = mn;
-                l[x] *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[x][d] *= f;
-            }
-            const float mx = m[x] == -__builtin_inff() ? 0.0f : m[x];
-            float w[8];
+            // score j is y[j] kr[j]; what the row does not see weighs 0, whatever its scales hold
+            float y[8], kr[8], sv[8], pv[8], sum;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                w[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], rq[x], -mx));
-                l[x] += w[j];
-                w[j] *= sv[j];
+                y[j] = s[x][j >> 2][j & 3];
+                kr[j] = kv_scale<FMT>(t.ks[j]) * rq[x];
+                sv[j] = kv_scale<FMT>(t.vs[j]);
             }
             if (!whole) {
-                // a weight of 0 on a scale that is not finite stays 0
+                uint32_t see = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = y[j] == -__builtin_inff() ? 0.0f : w[j];
+                for (int j = 0; j < 8; ++j)
+                    see |= (uint32_t)((t.there >> (j >> 2) & 1) && kv_sees(a, q, qi[x], first_token + (j & 3) + 16 * (j >> 2))) << j;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = see >> j & 1;
+                    y[j] = in ? y[j] : -__builtin_inff();
+                    kr[j] = in ? kr[j] : 1.0f;
+                    sv[j] = in ? sv[j] : 0.0f;
+                }
             }
+            for (bool moved = false;; moved = true) {
+                float top = 0.0f;
+                sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[x][j] = (_Float16)w[j];
+                for (int j = 0; j < 8; ++j) {
+                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], kr[j], -m[x]));
+                    pv[j] = w * (sv[j] * fb[x]);
+                    sum += w;
+                    top = __builtin_fmaxf(top, __builtin_fabsf(pv[j]));
+                }
+                if (moved || !__any((top > 0x1p15f) | (sum > kMaxWeight))) break;
+                float ty = m[x] + __builtin_amdgcn_logf(l[x]), tp = -__builtin_inff();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    ty = __builtin_fmaxf(ty, y[j] * kr[j]);
+                    tp = __builtin_fmaxf(tp, y[j] * kr[j] + scale_log2(sv[j]));
+                }
+#pragma unroll
+                for (int o = 16; o < 64; o <<= 1) {
+                    ty = __builtin_fmaxf(ty, __shfl_xor(ty, o, 64));
+                    tp = __builtin_fmaxf(tp, __shfl_xor(tp, o, 64));
+                }
+                const RowStep f = raise_row<7>(m[x], fb[x], ty, tp);
+                l[x] *= f.l;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[x][d] *= f.o;
+            }
+            l[x] += sum;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[x][j] = (_Float16)pv[j];
         }
         // O^T += V^T P^T
         uint32_t vz[4];
@@ -277,8 +265,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         }
     }
 
-    // join the waves, 16 rows at a time
-    const float unit = __uint_as_float((e_ref + 1u) << 23) * L::UNIT;
+    // join the waves, 16 rows at a time: each wave's result times its share of the sum
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
         l[x] += __shfl_xor(l[x], 16, 64);
@@ -289,30 +276,30 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
             l_lds[wave][r] = l[x];
         }
         __syncthreads();
-        float top = m_lds[0][r];
+        float base = m_lds[0][r], sum = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, m_lds[w][r]);
-        const float f = m[x] == -__builtin_inff() && l[x] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[x] - (top == -__builtin_inff() ? 0.0f : top)) * unit;
+        for (int w = 1; w < kWaves; ++w) base = __builtin_fmaxf(base, m_lds[w][r]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += l_lds[w][r] * __builtin_amdgcn_exp2f(m_lds[w][r] - base);
+        const float f = __builtin_amdgcn_exp2f(m[x] - base) / sum, unit = L::UNIT / fb[x];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int d = 0; d < DT; d += 4) {
                 float4_t y;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = f == 0.0f ? 0.0f : o[x][d + c][n] * f;
+                for (int c = 0; c < 4; ++c) y[c] = l[x] == 0.0f ? 0.0f : o[x][d + c][n] * f * unit;
                 *reinterpret_cast<float4_t*>(&o_lds[wave][r][(4 * g + n) * DT + d]) = y;
             }
         __syncthreads();
         const int row = r0 + 16 * x + threadIdx.x / 16, part = threadIdx.x % 16;
         if (row < rows) {
             const int rr = threadIdx.x / 16;
-            float best = m_lds[0][rr], sum = 0.0f;
+            float base = m_lds[0][rr], sum = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) best = __builtin_fmaxf(best, m_lds[w][rr]);
-            const float base = best == -__builtin_inff() ? 0.0f : best;
+            for (int w = 1; w < kWaves; ++w) base = __builtin_fmaxf(base, m_lds[w][rr]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                sum += l_lds[w][rr] == 0.0f ? 0.0f : l_lds[w][rr] * __builtin_amdgcn_exp2f(m_lds[w][rr] - base);
+            for (int w = 0; w < kWaves; ++w) sum += l_lds[w][rr] * __builtin_amdgcn_exp2f(m_lds[w][rr] - base);
             float y[DT];
 #pragma unroll
             for (int d = 0; d < DT; ++d) y[d] = 0.0f;
@@ -324,10 +311,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
 #pragma unroll
                     for (int c = 0; c < 4; ++c) y[d + c] += z[c];
                 }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t to = (q.q0 + row / G) * a.q_heads + h * G + row % G;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] * inv;
             const float ls = sum == 0.0f ? -__builtin_inff() : base + __builtin_log2f(sum);
             if (sp.splits > 1) {
                 float* to_o = po + ((int64_t)split * a.tokens * a.q_heads + to) * D + part * DT;
@@ -356,16 +340,18 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
     const bool there = row < (int64_t)q.len * a.q_heads;
     if (WPR == 1 && !there) return;
     const int64_t to = q.q0 * a.q_heads + (there ? row : 0), n = a.tokens * a.q_heads;
-    float top = -__builtin_inff();
-    if (there)
-        for (int s = lane; s < splits; s += 64) top = __builtin_fmaxf(top, pl[s * n + to]);
+    auto load = [&](int s) { return there && s < splits ? pl[s * n + to] : -__builtin_inff(); };
+    const float first = load(lane);
+    float top = first;
+    for (int s = lane + 64; s < splits; s += 64) top = __builtin_fmaxf(top, load(s));
     top = wave_max<64>(top);
     const float base = top == -__builtin_inff() ? 0.0f : top;
-    float y[E] = {}, sum = 0.0f;
+    float y[E] = {}, sum = __builtin_amdgcn_exp2f(first - base);
+    for (int s = lane + 64; s < splits; s += 64) sum += __builtin_amdgcn_exp2f(load(s) - base);
+    sum = wave_sum<64>(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     for (int s0 = 0; s0 < splits; s0 += 64) {
-        const float ls = there && s0 + lane < splits ? pl[(s0 + lane) * n + to] : -__builtin_inff();
-        const float w = __builtin_amdgcn_exp2f(ls - base);
-        sum += w;
+        const float w = __builtin_amdgcn_exp2f((s0 == 0 ? first : load(s0 + lane)) - base) * inv;
         const int last = splits - s0 < 64 ? splits - s0 : 64;
         for (int s = wave % WPR; s < last; s += 8 * WPR) {
             float p[8][E], ws[8];
@@ -383,7 +369,6 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
                 for (int d = 0; d < E; ++d) y[d] += ws[x] == 0.0f ? 0.0f : ws[x] * p[x][d];
         }
     }
-    sum = wave_sum<64>(sum);
     if constexpr (WPR > 1) {
 #pragma unroll
         for (int d = 0; d < E; ++d) part[wave][lane * E + d] = y[d];
@@ -394,8 +379,6 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
 #pragma unroll
             for (int d = 0; d < E; ++d) y[d] += part[w][lane * E + d];
     }
-#pragma unroll
-    for (int d = 0; d < E; ++d) y[d] = sum == 0.0f ? 0.0f : y[d] / sum;
     store_out<E>(a, to * D + lane * E, y);
     if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
 }

@@ -32,9 +32,12 @@
 // scaled by one power of two per block, not per row, so the score's factors fold
 // into the token's scale (a query element below 2^-30 of the largest of the
 // block's rows loses BF16 bits; its score then errs by 2^-38 of the largest |q| |k|
-// there at most).  The weights are taken against the running reference before
-// their maximum is known, and only if a lane's sum passes 2^8 is the maximum
-// found, the reference moved and the weights taken again.
+// there at most).  The weights are taken against the running references before
+// their maxima are known, and only if a lane's sum times the tile's largest value
+// scale passes 2^15 are the maxima found, the row's references moved and the weights
+// taken again; a wave that has a row with two references (raise_row in bg_kvattn.h:
+// value scales beyond 2^+-40) takes them so always.  A row's largest w s lies at 2^3
+// at least, so one that falls below FP16's normal range errs by 2^-28 of it.
 #include "bg_device.h"
 #include "bg_internal.h"
 #include "bg_kvattn.h"
@@ -57,8 +60,9 @@ struct ManyLds {
     static constexpr int KRING = D == 256 ? 4 : 8, VRING = D == 256 ? 5 : 8;       // of 5 and 6 needed at D <= 128, 8 cost no division
     half8_t k[KRING][D / 8][32];      // [step mod KRING][8 elements][token]
     half8_t v[VRING][2][2][D];        // [step mod VRING][16 tokens][lane half][element e of lane r at e LR + r]
-    float ks[4][kT], vs[4][kT];       // [tile mod 4]: key scales times the queries' unit, value scales over 2^(e - 126)
-    uint32_t e[4];                    // [tile mod 4]
+    float ks[4][kT], vs[4][kT];       // [tile mod 4]: key scales times the queries' unit, value scales
+    float lv[4][kT];                  // log2 of the value scales' magnitude
+    float most[4];                    // [tile mod 4]: sums of weights up to this stay in FP16's range with the tile's value scales
     uint32_t top[8];
     uint16_t vz[4][kT];               // 4 bits: -2^-9 times the zero-points of values, FP16
 };
@@ -144,8 +148,10 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     half8_t qf[ST];
     float unit_s = 0.0f;
     float16_t o[DT], s[2];
-    float nm = __builtin_inff(), l = 0.0f;             // minus the reference, the sum
-    uint32_t e_ref = 0, e_next = 0;                    // O is over 2^(e_ref - 126), the next tile's values over e_next's
+    // of the lane's row: its sum, weights over 2^m, weights times value scales over 2^m / fb;
+    // apart: some row of the wave has an fb other than 1
+    float m = kNoRef, fb = 1.0f, l = 0.0f;
+    bool apart = false;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = float16_t{} ;
 
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(j < FV ? fv[j % FV] : value(n, j), p[1][j / DT], o[j % DT], 0, 0, 0);
         p[1][0] = p[1][1] = half8_t{};
     };
-    auto attend = [&](int i, auto U, bool whole, uint64_t seen, auto&& beside) {
+    auto attend = [&](int i, auto U, bool whole, uint64_t seen, float most, auto&& beside) {
         constexpr int u = U();
         const int n = 2 * i + u;
         float sum = 0.0f;
@@ -207,13 +213,13 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             beside(x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], nm));
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], -m));
                 sum += w;
                 p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(w * vn[j]);
             }
             if (x < 3) __builtin_amdgcn_sched_barrier(0);
         }
-        const bool again = (uint32_t)!whole | (uint32_t)(__ballot(!(sum <= 256.0f)) != 0) | (uint32_t)(u == 1 && e_next != e_ref);
+        const bool again = (uint32_t)!whole | (uint32_t)apart | (uint32_t)(__ballot(!(sum <= most)) != 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(p[u][j]));
         kr = k_scale(n + 1, 0);
@@ -222,26 +228,25 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         if (again) {
             const uint32_t see = (uint32_t)(seen >> (32 * u + 4 * g));     // bit 8 (j / 4) + j % 4: the row sees k-slot j
             auto in = [&](int x, int j) { return see >> (8 * x + j) & 1; };
-            float top = -__builtin_inff();
+            float ty = -__builtin_inff(), tp = -__builtin_inff();
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float4_t kn = k_scale(n, x);
+                const float4_t kn = k_scale(n, x), lv = *reinterpret_cast<const float4_t*>(&lds.lv[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = in(x, j) ? __builtin_fmaxf(top, s[u][4 * x + j] * kn[j]) : top;
+                for (int j = 0; j < 4; ++j) {
+                    const float y = s[u][4 * x + j] * kn[j];
+                    ty = in(x, j) ? __builtin_fmaxf(ty, y) : ty;
+                    tp = in(x, j) ? __builtin_fmaxf(tp, y + lv[j]) : tp;
+                }
             }
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-            const float ref = top + nm > 4.0f || nm == __builtin_inff() ? __builtin_fminf(nm, -top) : nm;      // the reference only rises
-            float x = nm == __builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ref - nm), v = 1.0f;
-            nm = ref;
-            l *= x;
-            if (u == 1) {
-                // from here on values are over the next tile's scale
-                v = e_next - e_ref > 126u ? 0.0f : __uint_as_float((127u - (e_next - e_ref)) << 23);
-                x *= v;
-                e_ref = e_next;
-            }
+            ty = __builtin_fmaxf(ty, m + __builtin_amdgcn_logf(l));
+            ty = __builtin_fmaxf(ty, __shfl_xor(ty, 32, 64));
+            tp = __builtin_fmaxf(tp, __shfl_xor(tp, 32, 64));
+            const RowStep f = raise_row<4>(m, fb, ty, tp);
+            apart = __any(fb != 1.0f);
+            l *= f.l;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] *= x;
+            for (int d = 0; d < DT; ++d) o[d] *= f.o;
             sum = 0.0f;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -249,9 +254,9 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // what the row does not see weighs 0, whatever its scales hold
-                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], nm)) : 0.0f;
+                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], -m)) : 0.0f;
                     sum += w;
-                    p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * vn[j] * v : 0.0f);
+                    p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * (vn[j] * fb) : 0.0f);
                 }
             }
         }
@@ -325,8 +330,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     };
     // Wave 0: the records of token `lane`, with the keys.
     uint32_t k_rec = 0, v_rec = 0;
-    float sv_ref = 0.0f, f_ref = 0x1p126f;             // value scales below sv_ref fit the reference 2^(e_put - 126) = 1 / f_ref
-    uint32_t e_put = 0;
+    float top_v = 0.0f, most_v = 0.0f;                 // a power of two above the tile's value scales, 2^15 over it
     auto load_records = [&](uint32_t& kr, uint32_t& vr, int base, uint32_t page) {
         const uint64_t at = pages.at(page, base + lane, 4);
         load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + at, &kr);
@@ -334,19 +338,16 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     };
     auto store_records = [&](uint32_t kr, uint32_t vr, int i, uint64_t live) {
         vr = live >> lane & 1 ? kv_masked_record<FMT>(vr) : 0u;
-        const float sv = kv_scale<FMT>(vr);
-        if (__any(sv >= sv_ref)) {
-            uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(sv))) >> 23;
-            e = e > 252u ? 252u : e;
-            if (e > e_put || sv_ref == 0.0f) {
-                e_put = e;
-                f_ref = __uint_as_float((253u - e) << 23);
-                sv_ref = __uint_as_float((e + 1u) << 23);
-            }
+        const float sv = kv_scale<FMT>(vr), size = __builtin_fabsf(sv);
+        if (__any(size >= top_v) || !__any(size >= top_v * 0x1p-6f)) {
+            const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(size))) >> 23;
+            top_v = __uint_as_float((e < 254u ? e + 1u : 255u) << 23);
+            most_v = __builtin_fminf(0x1p15f / top_v, kMaxWeight);
         }
         lds.ks[i & 3][lane] = kv_scale<FMT>(kr) * unit_s;
-        lds.vs[i & 3][lane] = sv * f_ref;
-        lds.e[i & 3] = e_put;
+        lds.vs[i & 3][lane] = sv;
+        lds.lv[i & 3][lane] = scale_log2(sv);
+        lds.most[i & 3] = most_v;
         if constexpr (FMT == KV_U4) lds.vz[i & 3][lane] = __builtin_bit_cast(uint16_t, (_Float16)(__builtin_bit_cast(_Float16, (uint16_t)(vr >> 16)) * (_Float16)-0x1p-9f));
     };
 
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     }
     __syncthreads();
     start(0);
-    if (nt > 0) e_ref = __builtin_amdgcn_readfirstlane(lds.e[0]);
+    float most = lds.most[0];
     __syncthreads();
     for (int i = 0; i < nt; ++i) {
         // Into what the last tile left, beside the products: keys and records of tile i + 2,
@@ -415,18 +416,18 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         const int base = b0;
         const bool whole = (th0 == ~0ull) & wr.whole(base, kT);
         uint64_t seen = ~0ull;
-        const uint32_t e = lds.e[(i + 1) & 3];
+        const float next = lds.most[(i + 1) & 3];
         if (!whole) seen = seen_bits(a, q, qi, base, th0);
         if (has_rows) {
-            attend(i, std::integral_constant<int, 0>{}, whole, seen, carry_keys);
-            e_next = __builtin_amdgcn_readfirstlane(e);
-            attend(i, std::integral_constant<int, 1>{}, whole, seen, carry_values);
+            attend(i, std::integral_constant<int, 0>{}, whole, seen, most, carry_keys);
+            attend(i, std::integral_constant<int, 1>{}, whole, seen, most, carry_values);
         } else {
 #pragma unroll
             for (int x = 0; x < 4; ++x) carry_keys(x);
 #pragma unroll
             for (int x = 0; x < 4; ++x) carry_values(x);
         }
+        most = next;
         b0 = b1;
         b1 = b2;
         b2 = b3;
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     if (has_rows) finish(2 * nt - 1);
     l += __shfl_xor(l, 32, 64);
     if (!ok) return;
-    const float y0 = l == 0.0f ? 0.0f : __uint_as_float((e_ref + 1u) << 23) * L::UNIT / l;
-    const float ls = l == 0.0f ? -__builtin_inff() : __builtin_log2f(l) - nm;
+    const float inv = 1.0f / l, unit = L::UNIT / fb;
+    const float ls = l == 0.0f ? -__builtin_inff() : __builtin_log2f(l) + m;
     constexpr int HB = M::LR / 32, RUN = 4 * M::E;          // accumulator row m of O[e HB + x] is element e of lane 32 x + m
 #pragma unroll
     for (int x = 0; x < HB; ++x)
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < M::E; ++e) y[j * M::E + e] = l == 0.0f ? 0.0f : o[e * HB + x][4 * n + j] * y0;
+                for (int e = 0; e < M::E; ++e) y[j * M::E + e] = l == 0.0f ? 0.0f : o[e * HB + x][4 * n + j] * inv * unit;
             const int64_t d = to * D + (32 * x + 8 * n + 4 * g) * M::E;
             if (sp.splits > 1) {
                 float* p = po + (int64_t)split * a.tokens * a.q_heads * D + d;

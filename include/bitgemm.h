@@ -544,9 +544,11 @@ bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t 
  * drafted token e exactly where bit e % 64 of tree[t][e / 64] is set (itself
  * included); bits from 64 * tree_words on are 0.  window must be 0.
  *
- * Scores, softmax statistics and sums are binary32; softmax weights are
- * rounded to FP16 (relative to the largest of their row) for the matrix cores,
- * the result once to dtype.  Codes of visible slots must be finite (as
+ * Scores, softmax statistics and sums are binary32; each softmax weight times
+ * its value's scale is rounded to FP16 for the matrix cores, by 2^-11 of itself
+ * or 2^-28 of the largest such product that its query sees, whichever is more;
+ * the result is rounded once to dtype.  Nothing that a query does not see
+ * reaches its result.  Codes of visible slots must be finite (as
  * kv_cache_write leaves them); what no query of a sequence sees may hold
  * anything.
  *   q          element (t, h, i) at t * q_token_stride + h * q_head_stride + i;
