@@ -148,6 +148,12 @@ constexpr float kMaxWeight = 0x1p50f;
 // log2 of a scale's magnitude (infinities and NaN aside); those below binary32's normal range count as its least.
 __device__ __forceinline__ float scale_log2(float s) { return __builtin_fmaxf(__builtin_amdgcn_logf(__builtin_fabsf(s)), -126.0f); }
 
+// a b, not fused with what takes it.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+    return a * b;
+}
+
 struct RowStep {
     float l, o;                // what the move makes of the sum and of the outputs
 };

@@ -207,8 +207,11 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
                 float ty = m[x] + __builtin_amdgcn_logf(l[x]), tp = -__builtin_inff();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    ty = __builtin_fmaxf(ty, y[j] * kr[j]);
-                    tp = __builtin_fmaxf(tp, y[j] * kr[j] + scale_log2(sv[j]));
+                    // rounded, as the reference is: past 2^31 a product's last half step would be a weight of infinity
+                    y[j] = rounded_product(y[j], kr[j]);
+                    kr[j] = 1.0f;
+                    ty = __builtin_fmaxf(ty, y[j]);
+                    tp = __builtin_fmaxf(tp, y[j] + scale_log2(sv[j]));
                 }
 #pragma unroll
                 for (int o = 16; o < 64; o <<= 1) {

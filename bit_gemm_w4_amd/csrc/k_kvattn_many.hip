@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 const float4_t kn = k_scale(n, x), lv = *reinterpret_cast<const float4_t*>(&lds.lv[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float y = s[u][4 * x + j] * kn[j];
+                    const float y = rounded_product(s[u][4 * x + j], kn[j]);
                     ty = in(x, j) ? __builtin_fmaxf(ty, y) : ty;
                     tp = in(x, j) ? __builtin_fmaxf(tp, y + lv[j]) : tp;
                 }
@@ -253,8 +253,9 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 const float4_t kn = k_scale(n, x), vn = v_scale(n, x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    // what the row does not see weighs 0, whatever its scales hold
-                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], -m)) : 0.0f;
+                    // what the row does not see weighs 0, whatever its scales hold; scores are rounded, as the
+                    // reference is: past 2^31 a product's last half step would be a weight of infinity
+                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(rounded_product(s[u][4 * x + j], kn[j]) - m) : 0.0f;
                     sum += w;
                     p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * (vn[j] * fb) : 0.0f);
                 }

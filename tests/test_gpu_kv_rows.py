@@ -174,3 +174,15 @@ def test_negative_scales(ops, kernel, fmt):  # noqa: F811
     for n in (0, 1):
         _scales(c, n, lambda s: s * rng.choice([-1.0, 1.0], s.shape))
     check_rows(c, _run(ops, c, kernel))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", [30, 60, 90])
+def test_scores_past_the_integers_of_binary32(ops, kernel, fmt, size):  # noqa: F811
+    """Queries of 2^size: a row is its best token's value, never NaN."""
+    n = 6 if kernel == "few" else 150
+    c = _case(ops, kernel, fmt, "bf16", 1, 2, 128, 16, [n], [330], seed=46)
+    c.q *= 2.0 ** size
+    lse = torch.empty(n, 2, device="cuda")
+    check_rows(c, _run(ops, c, kernel, lse=lse), lse)
