@@ -339,44 +339,40 @@ __device__ __forceinline__ void load_queries(const KvAttnArgs& a, int64_t at, in
     }
 }
 
-// ... and to FP16, BF16 ones scaled by one power of two for the block of WAVES waves: its
-// largest element that is finite lands in [2^13, 2^14).
+// ... and to FP16, BF16 ones scaled by a power of two: the largest element of the block's
+// rows (WAVES waves; rows that hold an infinity or NaN aside) lands in [2^13, 2^14).  A row
+// that lies more than 2^8 below takes its own, and `own`, which its scores then lack, is
+// not 1: another row never costs it bits.
 template <int FMT, int D, int WAVES>
-__device__ __forceinline__ float scale_queries(const KvAttnArgs& a, int wave, uint32_t* lds, half8_t* f) {
+__device__ __forceinline__ float scale_queries(const KvAttnArgs& a, int wave, uint32_t* lds, half8_t* f, float& own) {
     constexpr int N = D / 16;
-    int e = 13;
+    int e = 13, block = 13;
     if (a.bf16) {
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < N; ++c) top = max_magnitude(top, max_magnitude(__builtin_bit_cast(uint4, f[c])));
+        top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        const uint32_t t = top >> 16 > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu;
+        const bool some = t != 0u && t < 0x7F80u;
+        e = scale_exponent(top);
+        uint32_t most = some ? (uint32_t)(e + 128) : 0u;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
-        if (__any((top >> 16) >= 0x7F80u || (top & 0xFFFFu) >= 0x7F80u)) {
-            // infinities or NaN: the largest of the others
-            top = 0;
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                const uint4 v = __builtin_bit_cast(uint4, f[c]);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t lo = w[k] & 0x7FFFu, hi = w[k] >> 16 & 0x7FFFu;
-                    top = max_magnitude(top, (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F80u ? hi : 0u) << 16);
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = (uint32_t)__shfl_xor((int)most, o, 64);
+            most = x > most ? x : most;
         }
-        if ((threadIdx.x & 63) == 0) lds[wave] = top;
+        if ((threadIdx.x & 63) == 0) lds[wave] = most;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) top = max_magnitude(top, lds[w]);
-        e = __builtin_amdgcn_readfirstlane(scale_exponent(top));
+        for (int w = 0; w < WAVES; ++w) most = lds[w] > most ? lds[w] : most;
+        block = __builtin_amdgcn_readfirstlane(most == 0u ? 13 : (int)most - 128);
+        e = !some || e >= block - 8 ? block : e < block - 126 ? block - 126 : e;
     }
+    own = __uint_as_float((uint32_t)(127 + e - block) << 23);
     const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
 #pragma unroll
     for (int c = 0; c < N; ++c) f[c] = query8<FMT>(a.bf16, __builtin_bit_cast(uint4, f[c]), up);
-    return query_unit<FMT, D>(a, e);
+    return query_unit<FMT, D>(a, block);
 }
 
 template <int N>

@@ -29,14 +29,14 @@
 //
 // Numerics as in the few-row kernel: codes exact in FP16, scales and statistics
 // in binary32.  Two things differ, both to spare vector instructions.  Queries are
-// scaled by one power of two per block, not per row, so the score's factors fold
-// into the token's scale (a query element below 2^-30 of the largest of the
-// block's rows loses BF16 bits; its score then errs by 2^-38 of the largest |q| |k|
-// there at most).  The weights are taken against the running references before
+// scaled by one power of two per block, so the score's factors fold into the token's
+// scale; a row that lies more than 2^8 below the block's largest keeps its own, and its
+// wave takes every tile's weights as a masked one's (a query element below 2^-22 of
+// its row's largest loses BF16 bits).  The weights are taken against the running references before
 // their maxima are known, and only if a lane's sum times the tile's largest value
 // scale passes 2^15 are the maxima found, the row's references moved and the weights
 // taken again; a wave that has a row with two references (raise_row in bg_kvattn.h:
-// value scales beyond 2^+-40) takes them so always.  A row's largest w s lies at 2^3
+// value scales beyond 2^+-40) takes them so always, too.  A row's largest w s lies at 2^3
 // at least, so one that falls below FP16's normal range errs by 2^-28 of it.
 #include "bg_device.h"
 #include "bg_internal.h"
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     float unit_s = 0.0f;
     float16_t o[DT], s[2];
     // of the lane's row: its sum, weights over 2^m, weights times value scales over 2^m / fb;
-    // apart: some row of the wave has an fb other than 1
-    float m = kNoRef, fb = 1.0f, l = 0.0f;
+    // own: what its scores lack (scale_queries); apart: some row of the wave has an fb or own other than 1
+    float m = kNoRef, fb = 1.0f, l = 0.0f, own = 1.0f;
     bool apart = false;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = float16_t{} ;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 const float4_t kn = k_scale(n, x), lv = *reinterpret_cast<const float4_t*>(&lds.lv[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float y = rounded_product(s[u][4 * x + j], kn[j]);
+                    const float y = rounded_product(s[u][4 * x + j], kn[j] * own);
                     ty = in(x, j) ? __builtin_fmaxf(ty, y) : ty;
                     tp = in(x, j) ? __builtin_fmaxf(tp, y + lv[j]) : tp;
                 }
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             ty = __builtin_fmaxf(ty, __shfl_xor(ty, 32, 64));
             tp = __builtin_fmaxf(tp, __shfl_xor(tp, 32, 64));
             const RowStep f = raise_row<4>(m, fb, ty, tp);
-            apart = __any(fb != 1.0f);
+            apart = __any((fb != 1.0f) | (own != 1.0f));
             l *= f.l;
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= f.o;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 for (int j = 0; j < 4; ++j) {
                     // what the row does not see weighs 0, whatever its scales hold; scores are rounded, as the
                     // reference is: past 2^31 a product's last half step would be a weight of infinity
-                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(rounded_product(s[u][4 * x + j], kn[j]) - m) : 0.0f;
+                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(rounded_product(s[u][4 * x + j], kn[j] * own) - m) : 0.0f;
                     sum += w;
                     p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * (vn[j] * fb) : 0.0f);
                 }
@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         // the step before the first: no weight, but products with its values are taken
         half8_t* before = &lds.v[39 % lds.VRING][0][0][0];
         for (int x = threadIdx.x; x < 4 * D; x += WAVES * 64) before[x] = half8_t{};
-        unit_s = scale_queries<FMT, D, WAVES>(a, wave, lds.top, qf);
+        unit_s = scale_queries<FMT, D, WAVES>(a, wave, lds.top, qf, own);
+        apart = __any(own != 1.0f);
         if (nt > 0) {
             if (wave == 0) {
                 store_records(r0k, r0v, 0, th0);

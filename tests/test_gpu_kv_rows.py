@@ -186,3 +186,30 @@ def test_scores_past_the_integers_of_binary32(ops, kernel, fmt, size):  # noqa: 
     c.q *= 2.0 ** size
     lse = torch.empty(n, 2, device="cuda")
     check_rows(c, _run(ops, c, kernel, lse=lse), lse)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ratio", [20, 40, 90])
+def test_queries_of_any_size_in_one_block(ops, kernel, fmt, D, ratio):  # noqa: F811
+    """Every third query is 2^ratio times the others, or 2^-ratio; some rows are zeros."""
+    n = 6 if kernel == "few" else 150
+    for sign in (1, -1):
+        c = _case(ops, kernel, fmt, "bf16", 1, 2, D, 16, [n], [330], seed=44)
+        c.q[::3] *= 2.0 ** (sign * ratio)
+        c.q[1, 0] = 0.0
+        lse = torch.empty(n, 2, device="cuda")
+        check_rows(c, _run(ops, c, kernel, lse=lse), lse)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_keeps_to_its_row(ops, kernel, bad):  # noqa: F811
+    c = _case(ops, kernel, FP8, "bf16", 1, 2, 128, 16, [6 if kernel == "few" else 150], [330], seed=45)
+    c.q[2, 1, 7] = bad
+    got = _run(ops, c, kernel)
+    assert got[2, 1].isnan().all()
+    c.q[2, 1] = 0.0
+    got[2, 1] = c.run(ops)[2, 1]
+    check_rows(c, got)
