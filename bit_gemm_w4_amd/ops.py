@@ -518,6 +518,15 @@ class KVCache:
                             ("pages", pages), ("page_size", page), ("kv_heads", heads), ("head_dim", dim)):
             object.__setattr__(self, name, value)
 
+    # Copies and pickles carry the fields alone: the descriptor of the new tensors is their own.
+    def __getstate__(self):
+        return self.k, self.v, self.k_scales, self.v_scales, self.format
+
+    def __setstate__(self, state):
+        for name, value in zip(("k", "v", "k_scales", "v_scales", "format"), state):
+            object.__setattr__(self, name, value)
+        self.__post_init__()
+
     @property
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scales, self.v_scales))

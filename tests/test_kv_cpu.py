@@ -226,3 +226,24 @@ def test_workspace_follows_the_split(L):
     one = need(tokens=1, batch=1, max_q=1, max_kv=131072)
     assert one > 0 and one % (32 * 129 * 4) == 0
     assert need(tokens=1, batch=1, max_q=1, max_kv=131072, window=4096) < one
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "copy", "pickle", "replace"])
+def test_a_copied_cache_describes_its_own_tensors(monkeypatch, how):
+    """The descriptor that the library reads holds the addresses of the copy's tensors."""
+    import copy
+    import dataclasses
+    import pickle
+    from bit_gemm_w4_amd import ops
+    monkeypatch.setattr(ops, "_ptr", lambda t: ctypes.c_void_p(t.data_ptr()))       # host tensors, never launched on
+    for fmt in (I8, FP8, U4):
+        a = ops.kv_cache(2, 16, 1, 64, fmt, device="cpu")
+        b = {"deepcopy": copy.deepcopy, "copy": copy.copy, "pickle": lambda c: pickle.loads(pickle.dumps(c)),
+             "replace": lambda c: dataclasses.replace(c, v=c.v.clone())}[how](a)
+        for c in (a, b):
+            d = Cache.from_address(c.address)
+            assert (d.k, d.v, d.k_scales, d.v_scales) == tuple(t.data_ptr() for t in (c.k, c.v, c.k_scales, c.v_scales))
+            assert (d.pages, d.page_size, d.kv_heads, d.head_dim, d.format) == (2, 16, 1, 64, fmt)
+        assert a.address != b.address and (b.v.data_ptr() != a.v.data_ptr()) == (how != "copy")
+        del a
+        assert Cache.from_address(b.address).v == b.v.data_ptr()
