@@ -38,6 +38,11 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
     return q;
 }
 
+// The sequence's rows of a kv head: those of its first max_q queries.
+__device__ __forceinline__ int kv_rows(const KvAttnArgs& a, const KvSeq& q) {
+    return (q.len < (int)a.max_q ? q.len : (int)a.max_q) * (a.q_heads / a.c.heads);
+}
+
 // Whether query i of the sequence sees position j < kv (its page aside).
 __device__ __forceinline__ bool kv_sees(const KvAttnArgs& a, const KvSeq& q, int i, int j) {
     if (a.tree) {

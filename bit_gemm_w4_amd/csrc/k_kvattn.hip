@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.c.heads, rb = blockIdx.x / a.c.heads, split = blockIdx.y, b = blockIdx.z;
     const KvSeq q = kv_seq(a, b);
-    const int G = a.q_heads / a.c.heads, rows = q.len * G, r0 = rb * 16 * RT;
+    const int G = a.q_heads / a.c.heads, rows = kv_rows(a, q), r0 = rb * 16 * RT;
     if (r0 >= rows) return;
     const int last = (rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1;
     const KvRange rg = kv_range<32>(a, q, r0 / G, last / G);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.y;
     const KvSeq q = kv_seq(a, b);
     const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
-    const bool there = row < (int64_t)q.len * a.q_heads;
+    const bool there = row < (int64_t)kv_rows(a, q) * a.c.heads;
     if (WPR == 1 && !there) return;
     const int64_t to = q.q0 * a.q_heads + (there ? row : 0), n = a.tokens * a.q_heads;
     auto load = [&](int s) { return there && s < splits ? pl[s * n + to] : -__builtin_inff(); };

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     const int h = blockIdx.x % a.c.heads, split = blockIdx.y, b = blockIdx.z;
     const int rb = gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads;     // the longest first
     const KvSeq q = kv_seq(a, b);
-    const int G = a.q_heads / a.c.heads, rows = q.len * G, r0 = rb * WAVES * kRows;
+    const int G = a.q_heads / a.c.heads, rows = kv_rows(a, q), r0 = rb * WAVES * kRows;
     if (r0 >= rows) return;
     const int last = (rows < r0 + WAVES * kRows ? rows : r0 + WAVES * kRows) - 1;
     const KvRange rg = kv_range<kT>(a, q, r0 / G, last / G);

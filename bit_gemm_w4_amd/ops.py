@@ -642,6 +642,8 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
     dt = _TORCH_DT.get(q.dtype)
     if dt not in (F16, BF16):
         raise ValueError(f"{fn}: q must be float16/bfloat16, got {q.dtype}")
+    if max_q_len is None:
+        max_q_len = 1 if cu_q is None else max(T, 1)
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
         raise ValueError(f"{fn}: block_table must be a contiguous int32 matrix [batch][pages of a sequence]")
     B, max_pages = block_table.shape
@@ -655,7 +657,8 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
             raise ValueError(f"{fn}: tree must be a contiguous int64 matrix [{T}][words]")
         words = tree.shape[1]
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=q.dtype, device=q.device)
+        new = torch.empty if T <= B * max_q_len else torch.zeros       # more rows than the call can write
+        out = new((T, heads, dim), dtype=q.dtype, device=q.device)
     elif out.shape != (T, heads, dim) or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError(f"{fn}: out must be a contiguous {(T, heads, dim)} of {q.dtype}")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
@@ -680,7 +683,7 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
 
 
 def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
-            cu_q: torch.Tensor | None = None, max_q_len: int = 1, *, max_kv_len: int = 0, window: int = 0, sinks: int = 0,
+            cu_q: torch.Tensor | None = None, max_q_len: int | None = None, *, max_kv_len: int = 0, window: int = 0, sinks: int = 0,
             scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention of ragged queries [T][q_heads][D] over the cache -> [T][q_heads][D].
@@ -691,7 +694,9 @@ def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens:
     as -1, holds nothing).  A query sees the positions up to its own; with a
     window only the last `window` of them and the first `sinks`.  A query that
     sees nothing gives zeros.  max_q_len and max_kv_len (0: the table's width)
-    are host-side bounds of the lengths.  scale None: D ** -0.5.  lse: float32
+    are host-side bounds of the lengths: a sequence's queries past max_q_len are
+    left alone, and without it (None) every sequence may own all T, which costs
+    speed with cu_q.  scale None: D ** -0.5.  lse: float32
     [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
     workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream."""
     if stream is not None:
@@ -718,9 +723,13 @@ def kv_attn_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
     return _kv_attn("kv_attn_tree", q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, 0, 0, scale, out, lse, ws)
 
 
-def kv_attn_workspace_bytes(q_shape, cache: KVCache, batch: int, max_pages: int, max_q_len: int = 1, max_kv_len: int = 0,
+def kv_attn_workspace_bytes(q_shape, cache: KVCache, batch: int, max_pages: int, max_q_len: int | None = None, max_kv_len: int = 0,
                             window: int = 0, sinks: int = 0, tree_words: int = 0) -> int:
-    """Bytes of the workspace that kv_attn (kv_attn_tree with tree_words > 0) needs for queries of q_shape."""
+    """Bytes of the workspace that kv_attn (kv_attn_tree with tree_words > 0) needs for queries of q_shape;
+    max_q_len None: with or without cu_q."""
+    if max_q_len is None:
+        bounds = {max(q_shape[0], 1)} | ({1} if q_shape[0] == batch else set())
+        return max(kv_attn_workspace_bytes(q_shape, cache, batch, max_pages, n, max_kv_len, window, sinks, tree_words) for n in bounds)
     return int(lib().kv_attn_workspace_bytes(_KV_ATTN.pack(
         cache.address, 0, 0, 0, 0, max_pages, 0, 256, 0, 0, 0, q_shape[0], batch, max_q_len, max_kv_len, window, sinks,
         q_shape[1], BF16, tree_words, 1.0)))

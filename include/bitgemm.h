@@ -557,7 +557,7 @@ bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t 
  *              are clamped to 0..tokens; rows of out that no sequence owns are
  *              left alone.
  *   max_q      at least every sequence's query count (host value: sizes the grid;
- *              later queries are left alone)
+ *              the rows of out and lse of later queries are left alone)
  *   max_kv     at least every kv_lens entry, or 0 for the block table's width:
  *              sizes the split over positions; a smaller value costs only speed
  *   kv_lens    clamped to 0 .. max_pages * page_size, which is at most 2^31 - 2^25
