@@ -624,7 +624,11 @@ _kv_workspaces: dict = {}
 
 
 def _kv_workspace(nbytes: int, device, stream: int) -> torch.Tensor:
-    """A workspace of at least nbytes, cached per device and stream."""
+    """A workspace of at least nbytes, cached per device and stream.  In a graph's
+    capture it is the graph's own, from its memory pool: graphs captured on one
+    stream may be replayed on several, beside eager work."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, stream)
     ws = _kv_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -698,7 +702,8 @@ def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens:
     left alone, and without it (None) every sequence may own all T, which costs
     speed with cu_q.  scale None: D ** -0.5.  lse: float32
     [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
-    workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream."""
+    workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream
+    (a captured graph: its own)."""
     if stream is not None:
         return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, out, lse, ws),
                           lambda: kv_attn(q, cache, block_table, kv_lens, cu_q, max_q_len, max_kv_len=max_kv_len, window=window,
