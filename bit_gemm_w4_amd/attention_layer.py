@@ -83,26 +83,35 @@ class AttentionLayer:
         """counts[b] further tokens of each sequence (a prompt's chunk; one each: a decode step)."""
         y, _, _ = self._attend(x, counts)
         self.lens = [n + c for n, c in zip(self.lens, counts)]
+        self.drafts = None                                  # their rows are overwritten
         return ops.gemm_w4a16(y.flatten(1), self.o)
 
     def check(self, x: torch.Tensor, parents: list[list[int]]) -> torch.Tensor:
         """Drafted tokens of each sequence as a tree: their rows lie behind the sequence until `accept`."""
         if self.window:
             raise ValueError("AttentionLayer: draft trees see the whole prefix: no window")
-        words = (max(len(p) for p in parents) + 63) // 64
+        words = max(1, (max(len(p) for p in parents) + 63) // 64)
         rows = [r + [0] * (words - len(r)) for p in parents for r in tree_bits(p)]
-        y, k, v = self._attend(x, [len(p) for p in parents], self._ints(rows, torch.int64))
-        self.drafts = (k, v, [len(p) for p in parents])
+        y, k, v = self._attend(x, [len(p) for p in parents], self._ints(rows, torch.int64).view(-1, words))
+        self.drafts = (k, v, [list(p) for p in parents])
         return ops.gemm_w4a16(y.flatten(1), self.o)
 
     def accept(self, branches: list[list[int]]) -> None:
-        """Keep one branch of the last `check` per sequence: its tokens move up behind the prefix."""
-        k, v, counts = self.drafts
+        """Keep one branch of the last `check` per sequence, from the prefix on (empty: none of its tokens): they move
+        up behind the prefix."""
+        if self.drafts is None:
+            raise ValueError("AttentionLayer: no checked drafts to accept from")
+        k, v, trees = self.drafts
+        if len(branches) != len(trees):
+            raise ValueError(f"AttentionLayer: {len(branches)} branches for {len(trees)} sequences")
         rows, slots, first = [], [], 0
-        for b, branch in enumerate(branches):
+        for b, (branch, parents) in enumerate(zip(branches, trees)):
+            for up, i in zip([-1, *branch], branch):
+                if not 0 <= i < len(parents) or parents[i] != up:
+                    raise ValueError(f"AttentionLayer: {list(branch)} is no branch of sequence {b}'s tree {parents}")
             rows += [first + i for i in branch]
             slots += self._slots(b, self.lens[b], len(branch))
-            first += counts[b]
+            first += len(parents)
         at = self._ints(rows, torch.int64)
         ops.kv_cache_write(k[at], v[at], self.cache, self._ints(slots, torch.int64))
         self.lens = [n + len(branch) for n, branch in zip(self.lens, branches)]
