@@ -200,26 +200,30 @@ void for_kv(int dt, int fmt, int dim, F&& f) {
     else on_fmt(std::integral_constant<int, DT_BF16>{});
 }
 
-// Tokens of a block: as many as give each thread a row (one token of many heads: several).
-int token_group(const KvCache& c) {
-    const int rows = kBlock / (c.dim / 8);
-    return c.heads < rows ? rows / c.heads : 1;
+// Tokens of a block: as many as give each thread a row (one token of many heads: several),
+// two from 2^23 on, since a launch holds less than 2^32 threads along an axis.
+int token_group(const KvCache& c, int64_t tokens) {
+    const int rows = kBlock / (c.dim / 8), group = c.heads < rows ? rows / c.heads : 1;
+    return group < 2 && tokens > (1 << 23) ? 2 : group;
 }
 
-dim3 grid_of(const KvCache& c, int64_t tokens) { return dim3((unsigned)((tokens + token_group(c) - 1) / token_group(c)), 2); }
+dim3 grid_of(const KvCache& c, int64_t tokens) {
+    const int group = token_group(c, tokens);
+    return dim3((unsigned)((tokens + group - 1) / group), 2);
+}
 
 }  // namespace
 
 const char* launch_kv_write(const KvCache& c, const KvRows& x, int dt, int64_t tokens, const int64_t* slots, hipStream_t s) {
     for_kv(dt, c.fmt, c.dim, [&](auto DT, auto FMT, auto D) {
-        k_kv_write<DT(), FMT(), D()><<<grid_of(c, tokens), kBlock, 0, s>>>(c, x, tokens, token_group(c), slots);
+        k_kv_write<DT(), FMT(), D()><<<grid_of(c, tokens), kBlock, 0, s>>>(c, x, tokens, token_group(c, tokens), slots);
     });
     return kname("k_kv_write", dt, c.fmt, c.dim);
 }
 
 const char* launch_kv_read(const KvCache& c, const int64_t* slots, int64_t tokens, int dt, void* k, void* v, hipStream_t s) {
     for_kv(dt, c.fmt, c.dim, [&](auto DT, auto FMT, auto D) {
-        k_kv_read<DT(), FMT(), D()><<<grid_of(c, tokens), kBlock, 0, s>>>(c, slots, tokens, token_group(c), k, v);
+        k_kv_read<DT(), FMT(), D()><<<grid_of(c, tokens), kBlock, 0, s>>>(c, slots, tokens, token_group(c, tokens), k, v);
     });
     return kname("k_kv_read", dt, c.fmt, c.dim);
 }
