@@ -597,6 +597,8 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torc
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError(f"{fn}: the last axis of k and v must be contiguous")
     _on_device(fn, cache, k, v, slots)
+    if T == 1 or cache.kv_heads == 1:        # an axis of one element may have any stride
+        ks, vs = ((0 if T == 1 else s[0], 0 if cache.kv_heads == 1 else s[1]) for s in (ks, vs))
     _check(lib().kv_cache_write(cache.address, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt,
                                 slots.data_ptr(), T, _raw_stream(cache.device.index)), fn)
 
@@ -673,8 +675,9 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
     L = lib()
     s = _raw_stream(cache.device.index)
     args = _KV_ATTN.pack(
-        cache.address, q.data_ptr(), q.stride(0), q.stride(1), block_table.data_ptr(), max_pages, kv_lens.data_ptr(),
-        0 if cu_q is None else cu_q.data_ptr(), 0 if tree is None else tree.data_ptr(), out.data_ptr(),
+        cache.address, q.data_ptr(), 0 if T == 1 else q.stride(0), 0 if heads == 1 else q.stride(1),
+        block_table.data_ptr(), max_pages, kv_lens.data_ptr(), 0 if cu_q is None else cu_q.data_ptr(),
+        0 if tree is None else tree.data_ptr(), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), T, B, max_q_len, max_kv_len, window, sinks, heads, dt, words,
         dim ** -0.5 if scale is None else scale)
     if ws is None:
