@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     const int row = w0 + r;
     const bool ok = row < rows;
     const int qi = (ok ? row : rows - 1) / G;
-    const int64_t to = (q.q0 + qi) * a.q_heads + h * G + (ok ? row % G : 0);
 
     half8_t qf[ST];
     float unit_s = 0.0f;
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         uint32_t k0[PARTS][M::KW], k1[PARTS][M::KW], z0[PARTS], z1[PARTS], v0[PARTS][8][M::VB < 4 ? 1 : M::VB / 4], r0k = 0, r0v = 0, r1k = 0, r1v = 0;
         const uint32_t p0 = nt > 0 ? find(b0) : 0, p1 = nt > 0 ? find(b1) : 0;
         if (nt > 0) pg2 = find(b2);
-        load_queries<D>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs, g, ok, qf);
+        load_queries<D>(a, (q.q0 + qi) * a.q_ts + (h * G + (ok ? row - qi * G : 0)) * a.q_hs, g, ok, qf);
         if (nt > 0) {
             load_keys(k0, z0, b0, p0);
             load_values(v0, b0, p0);
@@ -445,6 +444,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     if (has_rows) finish(2 * nt - 1);
     l += __shfl_xor(l, 32, 64);
     if (!ok) return;
+    const int64_t to = (q.q0 + qi) * a.q_heads + h * G + row - qi * G;      // here, and not two registers through the loop
     const float inv = 1.0f / l, unit = L::UNIT / fb;
     const float ls = l == 0.0f ? -__builtin_inff() : __builtin_log2f(l) + m;
     constexpr int HB = M::LR / 32, RUN = 4 * M::E;          // accumulator row m of O[e HB + x] is element e of lane 32 x + m
