@@ -247,3 +247,13 @@ def test_a_copied_cache_describes_its_own_tensors(monkeypatch, how):
         assert a.address != b.address and (b.v.data_ptr() != a.v.data_ptr()) == (how != "copy")
         del a
         assert Cache.from_address(b.address).v == b.v.data_ptr()
+
+
+def test_a_long_sequence_alone_needs_a_workspace(L):
+    c = cache(pages=100000, kv_heads=8)
+    a = attn(c, tokens=1, batch=1, max_q=1, cu_q=None, q_heads=32, max_pages=8192)
+    need = L.kv_attn_workspace_bytes(ctypes.addressof(a))
+    assert need > 0
+    assert L.kv_attn(ctypes.addressof(a), None, 0, None) == E_WS
+    assert L.kv_attn(ctypes.addressof(a), P, need - 1, None) == E_WS
+    assert L.kv_attn(ctypes.addressof(a), P + 8, need, None) == E_ALIGN
