@@ -302,19 +302,19 @@ __device__ __forceinline__ float query_unit(const KvAttnArgs& a, int e) {
     return a.scale * 0x1.715476p0f * KvLayout<FMT, D>::UNIT * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 }
 
-// The row's query fragments for lane group g of GROUPS, BF16 ones scaled by a power of
+// The row's query fragments for lane group g of four, BF16 ones scaled by a power of
 // two so that FP16 holds them; returns the factor that takes a product of
 // operands to a base-2 exponent.  Rows that are not there are zeros.
-template <int FMT, int D, int GROUPS>
+template <int FMT, int D>
 __device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int g, bool ok, half8_t* f) {
     using L = KvLayout<FMT, D>;
-    constexpr int N = D / (8 * GROUPS), CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;    // elements a lane holds in a run
+    constexpr int N = D / 32, CHUNK = FMT == KV_U4 ? 2 * L::KB : L::KB;    // elements a lane holds in a run
     uint4 w[N];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int in = i * 8 % CHUNK, c = i * 8 / CHUNK;
-        const int d = c * GROUPS * CHUNK + g * CHUNK + in;
+        const int d = c * 4 * CHUNK + g * CHUNK + in;
         w[i] = make_uint4(0, 0, 0, 0);
         if (ok) w[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
     }
@@ -323,7 +323,7 @@ __device__ __forceinline__ float load_query(const KvAttnArgs& a, int64_t at, int
 #pragma unroll
         for (int i = 0; i < N; ++i) top = max_magnitude(top, max_magnitude(w[i]));
 #pragma unroll
-        for (int o = 64 / GROUPS; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
+        for (int o = 16; o < 64; o <<= 1) top = max_magnitude(top, (uint32_t)__shfl_xor((int)top, o, 64));
         e = scale_exponent(top);
     }
     const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);

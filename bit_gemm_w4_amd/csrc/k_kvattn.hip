@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         const bool ok = row < rows;
         qi[x] = (ok ? row : rows - 1) / G;
         const int64_t at = (q.q0 + qi[x]) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs;
-        rq[x] = load_query<FMT, D, 4>(a, at, g, ok, qf[x]);
+        rq[x] = load_query<FMT, D>(a, at, g, ok, qf[x]);
         m[x] = kNoRef;
         l[x] = 0.0f;
         fb[x] = 1.0f;
