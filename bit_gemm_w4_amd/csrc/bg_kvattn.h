@@ -345,13 +345,13 @@ __device__ __forceinline__ void load_queries(const KvAttnArgs& a, int64_t at, in
 }
 
 // ... and to FP16, BF16 ones scaled by a power of two: the largest element of the block's
-// rows (WAVES waves; rows that hold an infinity or NaN aside) lands in [2^13, 2^14).  A row
-// that lies more than 2^8 below takes its own, and `own`, which its scores then lack, is
+// rows (WAVES waves; rows that hold an infinity or NaN aside) lands in [2^15, 2^16).  A row
+// that lies more than 2^16 below takes its own, and `own`, which its scores then lack, is
 // not 1: another row never costs it bits.
 template <int FMT, int D, int WAVES>
 __device__ __forceinline__ float scale_queries(const KvAttnArgs& a, int wave, uint32_t* lds, half8_t* f, float& own) {
     constexpr int N = D / 16;
-    int e = 13, block = 13;
+    int e = 15, block = 15;
     if (a.bf16) {
         uint32_t top = 0;
 #pragma unroll
@@ -370,14 +370,14 @@ __device__ __forceinline__ float scale_queries(const KvAttnArgs& a, int wave, ui
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) most = lds[w] > most ? lds[w] : most;
-        block = __builtin_amdgcn_readfirstlane(most == 0u ? 13 : (int)most - 128);
-        e = !some || e >= block - 8 ? block : e < block - 126 ? block - 126 : e;
+        block = __builtin_amdgcn_readfirstlane(most == 0u ? 15 : (int)most - 128);
+        e = !some || e >= block - 16 ? block : e < block - 126 ? block - 126 : e;
     }
     own = __uint_as_float((uint32_t)(127 + e - block) << 23);
-    const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+    const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
 #pragma unroll
     for (int c = 0; c < N; ++c) f[c] = query8<FMT>(a.bf16, __builtin_bit_cast(uint4, f[c]), up);
-    return query_unit<FMT, D>(a, block);
+    return query_unit<FMT, D>(a, block - 2);
 }
 
 template <int N>

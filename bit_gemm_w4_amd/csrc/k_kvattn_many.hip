@@ -30,12 +30,13 @@
 // Numerics as in the few-row kernel: codes exact in FP16, scales and statistics
 // in binary32.  Two things differ, both to spare vector instructions.  Queries are
 // scaled by one power of two per block, so the score's factors fold into the token's
-// scale; a row that lies more than 2^8 below the block's largest keeps its own, and its
-// wave takes every tile's weights as a masked one's (a query element below 2^-22 of
-// its row's largest loses BF16 bits).  The weights are taken against the running references before
-// their maxima are known, and only if a lane's sum times the tile's largest value
-// scale passes 2^15 are the maxima found, the row's references moved and the weights
-// taken again; a wave that has a row with two references (raise_row in bg_kvattn.h:
+// scale; a row that lies more than 2^16 below the block's largest keeps its own, and its
+// wave takes every tile's weights as a masked one's (twice the time; above that, a
+// query element errs by 2^-24 of its row's largest at most).  The weights are taken
+// against the running references before their maxima are known, and only if one of them
+// times its value's scale left FP16's range (which is looked at if a lane's sum times
+// the tile's largest value scale passes 2^15) are the maxima found, the row's references
+// moved and the weights taken again; a wave that has a row with two references (raise_row in bg_kvattn.h:
 // value scales beyond 2^+-40) takes them so always, too.  A row's largest w s lies at 2^3
 // at least, so one that falls below FP16's normal range errs by 2^-28 of it.
 #include "bg_device.h"
@@ -218,9 +219,17 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             }
             if (x < 3) __builtin_amdgcn_sched_barrier(0);
         }
-        const bool again = (uint32_t)!whole | (uint32_t)apart | (uint32_t)(__ballot(!(sum <= most)) != 0);
+        bool again = (uint32_t)!whole | (uint32_t)apart;
 #pragma unroll
         for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(p[u][j]));
+        if (__ballot(!(sum <= most)) != 0 && !again) {
+            // some product may have left FP16's range
+            const half8_t top = __builtin_elementwise_max(__builtin_elementwise_abs(p[u][0]), __builtin_elementwise_abs(p[u][1]));
+            bool left = sum > kMaxWeight;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) left |= top[j] == (_Float16)__builtin_inff();
+            again = __any(left);
+        }
         kr = k_scale(n + 1, 0);
         vr = v_scale(n + 1, 0);
         __builtin_amdgcn_sched_barrier(0);
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     auto store_records = [&](uint32_t kr, uint32_t vr, int i, uint64_t live) {
         vr = live >> lane & 1 ? kv_masked_record<FMT>(vr) : 0u;
         const float sv = kv_scale<FMT>(vr), size = __builtin_fabsf(sv);
-        if (__any(size >= top_v) || !__any(size >= top_v * 0x1p-6f)) {
+        if (__any(size >= top_v) || !__any(size >= top_v * 0x1p-3f)) {
             const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(size))) >> 23;
             top_v = __uint_as_float((e < 254u ? e + 1u : 255u) << 23);
             most_v = __builtin_fminf(0x1p15f / top_v, kMaxWeight);
