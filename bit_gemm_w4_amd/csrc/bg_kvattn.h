@@ -159,6 +159,20 @@ __device__ __forceinline__ float rounded_product(float a, float b) {
     return a * b;
 }
 
+// The record that kv_cache_write gives a row of zeros (scale 1, zero-point 0).  Its products
+// are 0 whatever the weight, so it must not raise a reference: next to a first token of
+// zeros that takes most of the weight, the others would fall below FP16's range.
+template <int FMT>
+__device__ __forceinline__ bool kv_maybe_zeros(uint32_t record) {
+    return record == (FMT == KV_U4 ? 0x3C00u : 0x3F800000u);
+}
+
+// Codes that are not 0 (E4M3: of either sign).
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_some(uint32_t codes) {
+    return FMT == KV_FP8 ? codes & 0x7F7F7F7Fu : codes;
+}
+
 struct RowStep {
     float l, o;                // what the move makes of the sum and of the outputs
 };

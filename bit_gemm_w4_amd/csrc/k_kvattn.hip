@@ -204,6 +204,24 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
                     top = __builtin_fmaxf(top, __builtin_fabsf(pv[j]));
                 }
                 if (moved || !__any((top > 0x1p15f) | (sum > kMaxWeight))) break;
+                uint32_t zeros = 0;           // bit j: k-slot j's value row may be of zeros
+#pragma unroll
+                for (int j = 0; j < 8; ++j) zeros |= (uint32_t)kv_maybe_zeros<FMT>(t.vs[j]) << j;
+                if (__any(zeros)) {
+                    uint32_t some = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t codes = 0;
+#pragma unroll
+                        for (int w = 0; w < L::VW; ++w) codes |= kv_some<FMT>(t.v[j][w]);
+                        some |= (uint32_t)(codes != 0u) << j;
+                    }
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) some |= (uint32_t)__shfl_xor((int)some, o, 64);
+                    zeros &= ~some;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sv[j] = zeros >> j & 1 ? 0.0f : sv[j];
+                }
                 float ty = m[x] + __builtin_amdgcn_logf(l[x]), tp = -__builtin_inff();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {

@@ -345,8 +345,18 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.ks) + at, &kr);
         load_bytes<4>(reinterpret_cast<const uint8_t*>(a.c.vs) + at, &vr);
     };
-    auto store_records = [&](uint32_t kr, uint32_t vr, int i, uint64_t live) {
+    auto store_records = [&](uint32_t kr, uint32_t vr, int i, uint64_t live, int base, uint32_t page) {
         vr = live >> lane & 1 ? kv_masked_record<FMT>(vr) : 0u;
+        if (__any(kv_maybe_zeros<FMT>(vr))) {
+            const uint8_t* row = a.c.v + pages.at(page, base + lane, L::ROW);
+            uint32_t some = 0;
+            for (int n = 0; n < L::ROW; n += 16) {
+                uint32_t w[4];
+                load_bytes<16>(row + n, w);
+                some |= kv_some<FMT>(w[0] | w[1] | w[2] | w[3]);
+            }
+            if (kv_maybe_zeros<FMT>(vr) && some == 0u) vr = 0u;
+        }
         const float sv = kv_scale<FMT>(vr), size = __builtin_fabsf(sv);
         if (__any(size >= top_v) || !__any(size >= top_v * 0x1p-3f)) {
             const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max<64>(size))) >> 23;
@@ -393,8 +403,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         apart = __any(own != 1.0f);
         if (nt > 0) {
             if (wave == 0) {
-                store_records(r0k, r0v, 0, th0);
-                store_records(r1k, r1v, 1, th1);
+                store_records(r0k, r0v, 0, th0, b0, p0);
+                store_records(r1k, r1v, 1, th1, b1, p1);
             }
             store_keys(k0, z0, 0);
             store_keys(k1, z1, 1);
@@ -418,7 +428,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             if (x == 2) load_values(vc, b2, pg2);
         };
         if (wave == 0) {
-            store_records(k_rec, v_rec, i + 2, th2);
+            store_records(k_rec, v_rec, i + 2, th2, b2, pg2);
             load_records(k_rec, v_rec, b3, pg3);
         }
         const uint64_t th3 = live_of(b3, pg3);

@@ -546,7 +546,8 @@ bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t 
  *
  * Scores, softmax statistics and sums are binary32; each softmax weight times
  * its value's scale is rounded to FP16 for the matrix cores, by 2^-11 of itself
- * or 2^-28 of the largest such product that its query sees, whichever is more;
+ * or 2^-28 of the largest such product that its query sees (of slots that
+ * kv_cache_write wrote as rows of zeros none counts), whichever is more;
  * the result is rounded once to dtype.  Nothing that a query does not see
  * reaches its result.  Codes of visible slots must be finite (as
  * kv_cache_write leaves them); what no query of a sequence sees may hold

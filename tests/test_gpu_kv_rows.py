@@ -6,7 +6,7 @@ The bound is taken row by row, over the tokens that the row sees:
 * the output's own rounding, u_out |y| (2^-8 BF16, 2^-11 FP16);
 * the rounding to FP16 of each weight times its value's scale, w s: 2^-11 relative, or, where it falls below
   FP16's normal range, half of FP16's last step.  The row's largest w s lies at 2^3 at least, so that step is
-  2^-24 / 2^3 of it and the error of a token 2^-28 max(w s) |code|;
+  2^-24 / 2^3 of it and the error of a token 2^-28 max(w s) |code|, rows of zeros aside;
 * binary32 scores and sums as in test_gpu_kv.py.
 
 Where a row sees a value whose scale is infinite, the result is infinite or NaN element by element, as in binary64.
@@ -55,7 +55,7 @@ def check_rows(c, got, lse=None, scale=None):
                     y = w @ v[at] / total
                     top = (np.abs(k[at]) @ np.abs(q[first + i, hq])).max() * scale
                     rel = (2 * (c.D + 16) * top + at.size + 16) * 2.0 ** -24
-                    lost = 2.0 ** -28 * (w * s_v[at]).max() * code[at].sum(0) / total
+                    lost = 2.0 ** -28 * (w * s_v[at] * code[at].any(1)).max() * code[at].sum(0) / total
                     tol = u_out * np.abs(y) + (1 + u_out) * ((2.0 ** -11 + rel) * (w @ np.abs(v[at]) / total) + lost)
                     tol = tol + (2.0 ** -25 if c.dtype == "f16" else 2.0 ** -133)
                     with np.errstate(invalid="ignore"):
@@ -121,12 +121,7 @@ def test_a_loud_value_stays_with_the_rows_that_see_it(ops, kernel, fmt, D, tree,
         check_rows(c, _run(ops, c, kernel, lse=lse), lse)
 
 
-@pytest.mark.parametrize("kernel", KERNELS)
-@pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("share", [0.9, 0.99, 0.9999])
-def test_a_first_token_that_takes_the_weight(ops, kernel, fmt, share):  # noqa: F811
-    """A long sequence whose first token has `share` of each row's weight and a value near zero: the others' small
-    weights make the result, in blocks that walk the whole sequence."""
+def _sink(ops, kernel, fmt, share):  # noqa: F811
     n, length, D = (1, 131072, 64) if kernel == "few" else (130, 40000, 64)
     rng = np.random.default_rng(3)
     c = Copies(ops, fmt, "f16", 1, 1, D, 128, [n], [length], seed=41)
@@ -139,6 +134,16 @@ def test_a_first_token_that_takes_the_weight(ops, kernel, fmt, share):  # noqa: 
     c.code[0], c.scale[0], c.zero[0] = code, s, z
     c.cache.k.copy_(torch.from_numpy(ref.pack_u4(code) if fmt == U4 else code))
     c.cache.k_scales.copy_(torch.from_numpy(_records(s, z, fmt)))
+    return c
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("share", [0.9, 0.99, 0.9999])
+def test_a_first_token_that_takes_the_weight(ops, kernel, fmt, share):  # noqa: F811
+    """A long sequence whose first token has `share` of each row's weight and a value near zero: the others' small
+    weights make the result, in blocks that walk the whole sequence."""
+    c = _sink(ops, kernel, fmt, share)
     at = _token(c, 0, 0)
 
     def hush(s):
@@ -213,3 +218,44 @@ def test_a_query_that_is_not_finite_keeps_to_its_row(ops, kernel, bad):  # noqa:
     c.q[2, 1] = 0.0
     got[2, 1] = c.run(ops)[2, 1]
     check_rows(c, got)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("share", [0.5, 0.99])
+def test_a_first_token_of_zeros_that_takes_the_weight(ops, kernel, fmt, share):  # noqa: F811
+    """Its value is written as codes 0 with scale 1, far above the others' scales."""
+    c = _sink(ops, kernel, fmt, share)
+    _scales(c, 1, lambda s: s * 2.0 ** -6)
+    at, pages = _token(c, 0, 0), c.cache
+    zeros = torch.zeros(1, 1, c.D, device="cuda")
+    keep = pages.k.clone(), pages.k_scales.clone()
+    if fmt == FP8:
+        zeros[..., ::3] = -0.0                       # E4M3 has two zeros
+    ops.kv_cache_write(zeros, zeros, pages, torch.tensor([int(at[0]) * c.page + at[2]]).cuda())
+    pages.k.copy_(keep[0])
+    pages.k_scales.copy_(keep[1])
+    c.code[1][at], c.scale[1][at], c.zero[1][at] = 0, 1.0, 0.0
+    check_rows(c, _run(ops, c, kernel))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_of_one_and_rows_of_zeros(ops, kernel, fmt, D):  # noqa: F811
+    """Every scale is 1: some rows are zeros, the others are not."""
+    c = _case(ops, kernel, fmt, "f16", 1, 4, D, 16, [5 if kernel == "few" else 40], [300], seed=47)
+    _scales(c, 1, lambda s: np.ones_like(s))
+    rng = np.random.default_rng(5)
+    rows = rng.random(c.scale[1].shape) < 0.4
+    if fmt == U4:
+        rows_z = rng.random(c.scale[1].shape) < 0.5                      # a zero-point of 0 leaves codes that are not
+        c.zero[1] = np.where(rows | rows_z, 0.0, c.zero[1]).astype(np.float32)
+        live = c.cache.v_scales[..., 0].cpu().numpy() == 1.0
+        z = c.cache.v_scales[..., 1].cpu().numpy()
+        c.cache.v_scales[..., 1] = torch.from_numpy(np.where(live, c.zero[1], z).astype(np.float16)).cuda()
+    c.code[1] = np.where(rows[..., None], 0, c.code[1]).astype(c.code[1].dtype)
+    code = c.cache.v.cpu().numpy()
+    code[rows] = 0
+    c.cache.v.copy_(torch.from_numpy(code))
+    check_rows(c, _run(ops, c, kernel))
