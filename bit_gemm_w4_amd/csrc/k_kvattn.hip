@@ -85,6 +85,10 @@ template <int FMT, int D, int RT>
 __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     constexpr int DT = D / 16, ST = D / 32, PAD = D + 4;
+    // One tile in flight, not two; there a branch spares the products' 8 multiplications by fb for each
+    // 16 rows, 2 to 4 % (48 rows of 64 x 2000 tokens 83 -> 79 us).  With two tiles its code costs more
+    // than it spares (8 x 24-token trees in 4 bits, D = 64: 29.2 -> 29.9).
+    constexpr bool kOne = RT * D > 128;
     __shared__ float o_lds[kWaves][16][PAD];
     __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
 
@@ -126,6 +130,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     half8_t qf[RT][ST];
     // of each row: weights are over 2^m, weights times value scales over 2^m / fb
     float rq[RT], m[RT], l[RT], fb[RT];
+    bool apart = false;                   // some fb is not 1
     int qi[RT];
     float4_t o[RT][DT];
 #pragma unroll
@@ -199,9 +204,17 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(y[j], kr[j], -m[x]));
-                    pv[j] = w * (sv[j] * fb[x]);
+                    pv[j] = kOne ? w * sv[j] : w * (sv[j] * fb[x]);
                     sum += w;
-                    top = __builtin_fmaxf(top, __builtin_fabsf(pv[j]));
+                    if constexpr (!kOne) top = __builtin_fmaxf(top, __builtin_fabsf(pv[j]));
+                }
+                if constexpr (kOne) {
+                    if (apart) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pv[j] *= fb[x];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(pv[j]));
                 }
                 if (moved || !__any((top > 0x1p15f) | (sum > kMaxWeight))) break;
                 uint32_t zeros = 0;           // bit j: k-slot j's value row may be of zeros
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
                     tp = __builtin_fmaxf(tp, __shfl_xor(tp, o, 64));
                 }
                 const RowStep f = raise_row<7>(m[x], fb[x], ty, tp);
+                apart = apart || __any(fb[x] != 1.0f);
                 l[x] *= f.l;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[x][d] *= f.o;
@@ -256,11 +270,11 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         }
     };
 
-    if constexpr (RT * D > 128) {
+    if constexpr (kOne) {
         // One tile at a time leaves registers for two waves a SIMD, which cover each other's
-        // waits: 64 rows of 16 x 8192 tokens, E4M3, D = 128, 92 us with two tiles and one wave,
-        // 77 so; 48 rows of 64 x 2000, INT8, 114 and 78; 18 x 2 queries of 4668, 4 bits,
-        // D = 256, 59 and 46.
+        // waits: 64 rows of 16 x 8192 tokens (ragged, as below), E4M3, D = 128, 110 us with two
+        // tiles and one wave, 184 with two of each (spills), 82 so; 48 rows of 64 x 2000, INT8,
+        // 113, 172 and 79; 18 x 2 queries of 4668, 4 bits, D = 256, 55, 44 and 45.
         Tile<FMT, D> t;
         for (; i < t1; i += kWaves) {
             t.load(a, pa, h, rg.tile(i), r, g);
