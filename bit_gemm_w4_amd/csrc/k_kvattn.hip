@@ -12,10 +12,10 @@
 //   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = 16 tokens' codes, B = 16 rows
 //   O^T += V^T P^T  the same instruction, A = 16 head elements of 32 tokens
 // The tile's pages are looked up two tiles ahead; 8 waves a CU with two tiles each
-// keep about 130 KB of codes in flight, and 8-bit caches stream at 5.2 TB/s (decode
-// of 32 x 8192 tokens, 554 MB: 106 us; a large copy runs at 4.8 TB/s).  4 bits
+// keep about 130 KB of codes in flight, and 8-bit caches stream at 5.4 TB/s (decode
+// of 32 x 8192 tokens, 554 MB: 103 us; a large copy runs at 4.8 TB/s).  4 bits
 // have half the bytes for the same instructions: 4 x 131072 tokens 571 MB in
-// 117 us, 4.9 TB/s, and a block's start (6 us) weighs more.
+// 114 us, 5.0 TB/s, and a block's start (6 us) weighs more.
 //
 // The accumulator of S^T holds, in lane (row r, g), tokens 4 g .. 4 g + 3 of
 // each 16; those of two S^T tiles are exactly the 8 k-slots that lane feeds to

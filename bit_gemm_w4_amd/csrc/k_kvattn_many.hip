@@ -25,7 +25,9 @@
 // over a window of 4,096 in E4M3 (8 kv heads of 4, D = 128): 165 us, 835 TFLOP/s; the
 // few-row kernel takes 460 us, a library product of 8192^3 in FP16 runs at 1,064
 // TFLOP/s.  In 16x16x32, a barrier and codes of a tile at a time: 245 us; with half of
-// the waves carrying keys and half values outside the products: 175 us.
+// the waves carrying keys and half values outside the products: 175 us.  At D = 128 a
+// lane's 256 registers are full and 9 to 20 more lie in scratch, of what the loop seldom
+// asks for.
 //
 // Numerics as in the few-row kernel: codes exact in FP16, scales and statistics
 // in binary32.  Two things differ, both to spare vector instructions.  Queries are
@@ -33,12 +35,13 @@
 // scale; a row that lies more than 2^16 below the block's largest keeps its own, and its
 // wave takes every tile's weights as a masked one's (twice the time; above that, a
 // query element errs by 2^-24 of its row's largest at most).  The weights are taken
-// against the running references before their maxima are known, and only if one of them
-// times its value's scale left FP16's range (which is looked at if a lane's sum times
-// the tile's largest value scale passes 2^15) are the maxima found, the row's references
-// moved and the weights taken again; a wave that has a row with two references (raise_row in bg_kvattn.h:
-// value scales beyond 2^+-40) takes them so always, too.  A row's largest w s lies at 2^3
-// at least, so one that falls below FP16's normal range errs by 2^-28 of it.
+// against the running references before their maxima are known, and only if one of
+// them times its value's scale left FP16's range (which is looked at if a lane's sum
+// times the tile's largest value scale passes 2^15) are the maxima found, the row's
+// references moved and the weights taken again; a wave that has a row with two
+// references (raise_row in bg_kvattn.h: value scales beyond 2^+-40) takes them so
+// always, too.  A row's largest w s lies at 2^3 at least, so one that falls below
+// FP16's normal range errs by 2^-28 of it.
 #include "bg_device.h"
 #include "bg_internal.h"
 #include "bg_kvattn.h"

@@ -15,9 +15,10 @@
 // Quotients are taken through the row's reciprocal with Markstein's correction,
 // rows are found without a 64-bit division, and a row's lanes exchange without
 // LDS: with divisions for the first two and LDS for the third, 16,383 tokens of
-// 8 heads of 128 in E4M3 took 38 us to write, 22 now (101 MB at 4.5 TB/s; reading
-// them back 19 us at 5.3 TB/s; a large copy runs at 4.8).  4 bits at 4 heads of 256
-// are bound by the vector units still: 16,000 tokens 29 us, 2.8 TB/s.
+// 8 heads of 128 in E4M3 took 38 us to write with the rows in the last-level cache,
+// 22 now; 27 from memory (101 MB at 3.8 TB/s; reading them back 19 us at 5.3 TB/s; a
+// large copy runs at 4.8).  4 bits at 4 heads of 256 are bound by the vector units
+// still: 16,000 tokens 29 us, 2.8 TB/s.
 #include "bg_device.h"
 #include "bg_internal.h"
 #include "bg_kv.h"
