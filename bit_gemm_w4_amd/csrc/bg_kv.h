@@ -47,6 +47,7 @@ struct KvAttnArgs {
     const int32_t* kv_lens;    // [batch]
     const int32_t* cu_q;       // [batch + 1], or NULL: sequence b owns query b
     int64_t batch, max_q, max_kv;
+    int64_t chunk;             // queries of a sequence that its own blocks take, if not max_q (0); set by launch_kv_attn
     int64_t window, sinks;     // window 0: every earlier token is visible
     const uint64_t* tree;      // [tokens][tree_words] ancestor bits, or NULL: causal
     int tree_words;

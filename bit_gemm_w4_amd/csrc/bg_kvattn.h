@@ -43,6 +43,43 @@ __device__ __forceinline__ int kv_rows(const KvAttnArgs& a, const KvSeq& q) {
     return (q.len < (int)a.max_q ? q.len : (int)a.max_q) * (a.q_heads / a.c.heads);
 }
 
+// The rows r0 .. rows - 1 of sequence b, of which a block takes its first.
+struct KvBlock {
+    int b, r0, rows;
+    KvSeq q;
+};
+
+// Row block rb of blockIdx.z: of sequence z, of its first `chunk` queries if that is set; past
+// the batch, of those queries from `chunk` on whose sequence holds token (z - batch) chunk,
+// up to the next such token.  Between two such tokens no sequence has queries from `chunk`
+// on but the one that holds the first.  False: none.
+__device__ __forceinline__ bool kv_block(const KvAttnArgs& a, int rb, int per_block, KvBlock& o) {
+    const int G = a.q_heads / a.c.heads, z = blockIdx.z;
+    if (z < (int)a.batch) {
+        o.b = z;
+        o.q = kv_seq(a, z);
+        o.rows = kv_rows(a, o.q);
+        if (a.chunk && o.rows > (int)a.chunk * G) o.rows = (int)a.chunk * G;
+        o.r0 = rb * per_block;
+    } else {
+        const int64_t t = (z - a.batch) * a.chunk;
+        int low = 0, high = (int)a.batch - 1;              // the last sequence that starts at t or before
+        while (low < high) {
+            const int mid = (low + high + 1) >> 1;
+            if (a.cu_q[mid] <= t) low = mid;
+            else high = mid - 1;
+        }
+        o.b = low;
+        o.q = kv_seq(a, low);
+        const int64_t at = t - o.q.q0;
+        if (at < 0 || at >= o.q.len) return false;
+        const int64_t first = at < a.chunk ? a.chunk : at, end = at + a.chunk < o.q.len ? at + a.chunk : o.q.len;
+        o.rows = (int)end * G;
+        o.r0 = (int)first * G + rb * per_block;
+    }
+    return o.r0 < o.rows;
+}
+
 // Whether query i of the sequence sees position j < kv (its page aside).
 __device__ __forceinline__ bool kv_sees(const KvAttnArgs& a, const KvSeq& q, int i, int j) {
     if (a.tree) {
@@ -429,6 +466,11 @@ void for_format(int fmt, int dim, F&& f) {
     else if (fmt == KV_FP8) on_dim(std::integral_constant<int, KV_FP8>{});
     else on_dim(std::integral_constant<int, KV_U4>{});
 }
+
+constexpr int64_t kGridZ = 65535;        // blocks along the grid's third axis
+
+// Sequences, and the tokens past the batch of kv_block.
+inline unsigned kv_grid_z(const KvAttnArgs& a) { return (unsigned)(a.batch + (a.chunk ? (a.tokens + a.chunk - 1) / a.chunk : 0)); }
 
 // Many query rows per kv head, rows of row_blocks blocks of 8 waves (4 at D = 256; either at D = 64) (k_kvattn_many.hip).
 const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s);

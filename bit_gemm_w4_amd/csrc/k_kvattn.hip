@@ -94,10 +94,11 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
 
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = blockIdx.x % a.c.heads, rb = blockIdx.x / a.c.heads, split = blockIdx.y, b = blockIdx.z;
-    const KvSeq q = kv_seq(a, b);
-    const int G = a.q_heads / a.c.heads, rows = kv_rows(a, q), r0 = rb * 16 * RT;
-    if (r0 >= rows) return;
+    const int h = blockIdx.x % a.c.heads, split = blockIdx.y;
+    KvBlock own;
+    if (!kv_block(a, blockIdx.x / a.c.heads, 16 * RT, own)) return;
+    const KvSeq q = own.q;
+    const int G = a.q_heads / a.c.heads, rows = own.rows, r0 = own.r0, b = own.b;
     const int last = (rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1;
     const KvRange rg = kv_range<32>(a, q, r0 / G, last / G);
     const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
@@ -364,58 +365,63 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
 // Joins the splits of a row: o = sum_s 2^(ls_s - max) o_s / sum_s 2^(ls_s - max).
 // WPR waves take a row's splits in turn (64 splits one after the other: 18 us), eight
 // partials in flight each.  A split without tokens wrote no partial: its weight is 0
-// and what lies there is not used.
-template <int D, int WPR>
+// and what lies there is not used.  TURNS: the grid counts on fewer queries than a
+// sequence may have, so its rows come in turns.
+template <int D, int WPR, bool TURNS>
 __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, const float* po, const float* pl) {
     __shared__ float part[WPR == 1 ? 1 : 4][D];
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.y;
     const KvSeq q = kv_seq(a, b);
-    const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
-    const bool there = row < (int64_t)kv_rows(a, q) * a.c.heads;
-    if (WPR == 1 && !there) return;
-    const int64_t to = q.q0 * a.q_heads + (there ? row : 0), n = a.tokens * a.q_heads;
-    auto load = [&](int s) { return there && s < splits ? pl[s * n + to] : -__builtin_inff(); };
-    const float first = load(lane);
-    float top = first;
-    for (int s = lane + 64; s < splits; s += 64) top = __builtin_fmaxf(top, load(s));
-    top = wave_max<64>(top);
-    const float base = top == -__builtin_inff() ? 0.0f : top;
-    float y[E] = {}, sum = __builtin_amdgcn_exp2f(first - base);
-    for (int s = lane + 64; s < splits; s += 64) sum += __builtin_amdgcn_exp2f(load(s) - base);
-    sum = wave_sum<64>(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int s0 = 0; s0 < splits; s0 += 64) {
-        const float w = __builtin_amdgcn_exp2f((s0 == 0 ? first : load(s0 + lane)) - base) * inv;
-        const int last = splits - s0 < 64 ? splits - s0 : 64;
-        for (int s = wave % WPR; s < last; s += 8 * WPR) {
-            float p[8][E], ws[8];
+    const int64_t n = a.tokens * a.q_heads, rows = (int64_t)kv_rows(a, q) * a.c.heads, first_row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
+    int64_t row = first_row;
+    if (row >= rows) return;
+    do {
+        const int64_t to = q.q0 * a.q_heads + row;
+        auto load = [&](int s) { return s < splits ? pl[s * n + to] : -__builtin_inff(); };
+        const float first = load(lane);
+        float top = first;
+        for (int s = lane + 64; s < splits; s += 64) top = __builtin_fmaxf(top, load(s));
+        top = wave_max<64>(top);
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+        float y[E] = {}, sum = __builtin_amdgcn_exp2f(first - base);
+        for (int s = lane + 64; s < splits; s += 64) sum += __builtin_amdgcn_exp2f(load(s) - base);
+        sum = wave_sum<64>(sum);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int s0 = 0; s0 < splits; s0 += 64) {
+            const float w = __builtin_amdgcn_exp2f((s0 == 0 ? first : load(s0 + lane)) - base) * inv;
+            const int last = splits - s0 < 64 ? splits - s0 : 64;
+            for (int s = wave % WPR; s < last; s += 8 * WPR) {
+                float p[8][E], ws[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int sx = s + x * WPR < last ? s + x * WPR : s;
-                ws[x] = s + x * WPR < last ? __shfl(w, sx, 64) : 0.0f;
-                const float* at = po + ((int64_t)(s0 + sx) * n + to) * D + lane * E;
+                for (int x = 0; x < 8; ++x) {
+                    const int sx = s + x * WPR < last ? s + x * WPR : s;
+                    ws[x] = s + x * WPR < last ? __shfl(w, sx, 64) : 0.0f;
+                    const float* at = po + ((int64_t)(s0 + sx) * n + to) * D + lane * E;
 #pragma unroll
-                for (int d = 0; d < E; ++d) p[x][d] = at[d];
+                    for (int d = 0; d < E; ++d) p[x][d] = at[d];
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+#pragma unroll
+                    for (int d = 0; d < E; ++d) y[d] += ws[x] == 0.0f ? 0.0f : ws[x] * p[x][d];
             }
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-#pragma unroll
-                for (int d = 0; d < E; ++d) y[d] += ws[x] == 0.0f ? 0.0f : ws[x] * p[x][d];
         }
-    }
-    if constexpr (WPR > 1) {
+        if constexpr (WPR > 1) {
+            // WPR = 4: the block's waves share the row and its turns
+            if (TURNS && row > first_row) __syncthreads();
 #pragma unroll
-        for (int d = 0; d < E; ++d) part[wave][lane * E + d] = y[d];
-        __syncthreads();
-        if (wave > 0 || !there) return;
+            for (int d = 0; d < E; ++d) part[wave][lane * E + d] = y[d];
+            __syncthreads();
+            if (wave > 0) continue;
 #pragma unroll
-        for (int w = 1; w < 4; ++w)
+            for (int w = 1; w < 4; ++w)
 #pragma unroll
-            for (int d = 0; d < E; ++d) y[d] += part[w][lane * E + d];
-    }
-    store_out<E>(a, to * D + lane * E, y);
-    if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
+                for (int d = 0; d < E; ++d) y[d] += part[w][lane * E + d];
+        }
+        store_out<E>(a, to * D + lane * E, y);
+        if (a.lse && lane == 0) a.lse[to] = sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0x1.62e43p-1f;
+    } while (TURNS && (row += (int64_t)gridDim.x * (4 / WPR)) < rows);
 }
 
 // The kernel, rows of a block, and how positions are split over blocks.
@@ -423,9 +429,16 @@ struct Plan {
     int waves;                            // of a block of the many-row kernel; 0: the few-row kernel
     int rt;
     unsigned row_blocks;
+    int64_t chunk;                        // KvAttnArgs::chunk
     KvSplit sp;
     double us;
 };
+
+// Queries a sequence is taken to have: the bound, or where that is all of the call's and so
+// says nothing of one sequence, their mean; further ones are found by the blocks past
+// the batch (kv_block).  With a grid for the bound itself, a decode step of 32 x 8192
+// tokens that gave none took 237 us (81 with one), and 64 x 2000 206 (37).
+int64_t usual_q(const KvAttnArgs& a) { return a.batch > 1 && a.max_q == a.tokens ? (a.tokens + a.batch - 1) / a.batch : a.max_q; }
 
 // The plan with one of the kernels that takes the least time by this model: rounds of the
 // blocks that the device holds at once, each a start and its tiles; the join; and the
@@ -436,20 +449,28 @@ struct Plan {
 // D = 256, in 64 (47).
 Plan plan_with(const KvAttnArgs& a, int waves) {
     Plan p;
-    const int64_t rows = a.max_q * (a.q_heads / a.c.heads);
+    const int64_t G = a.q_heads / a.c.heads, usual = usual_q(a), rows = usual * G;
     const bool many = waves > 0, wide = a.c.dim == 256, narrow = a.c.dim == 64;
     p.waves = waves;
     p.rt = rows <= 16 || wide ? 1 : 2;
     const int per_block = many ? 32 * waves : 16 * p.rt, tile = many ? 64 : 32;
-    p.row_blocks = (unsigned)((rows + per_block - 1) / per_block);
+    p.chunk = 0;
+    if (usual < a.max_q && a.batch < kGridZ) {
+        // a block's queries at least, and as many as keep the blocks past the batch within the grid
+        const int64_t least = (a.tokens + kGridZ - a.batch - 1) / (kGridZ - a.batch);
+        p.chunk = usual > per_block / G ? usual : per_block / G;
+        p.chunk = p.chunk > least ? p.chunk : least;
+        if (p.chunk >= a.max_q) p.chunk = 0;
+    }
+    p.row_blocks = (unsigned)(((p.chunk ? p.chunk : a.max_q) * G + per_block - 1) / per_block);
     // positions a row block can see, in tiles
     int64_t seen = a.max_kv;
     if (a.window) {
-        const int64_t most = a.window + a.max_q + 64 + (a.sinks ? a.sinks + 64 : 0);
+        const int64_t most = a.window + (p.chunk ? p.chunk : a.max_q) + 64 + (a.sinks ? a.sinks + 64 : 0);
         seen = most < seen ? most : seen;
     }
     const int64_t tiles = (seen + tile - 1) / tile > 0 ? (seen + tile - 1) / tile : 1;
-    const int64_t blocks = a.batch * a.c.heads * p.row_blocks, room = many && (waves == 8 || wide) ? 256 : 512;
+    const int64_t blocks = a.batch * a.c.heads * ((rows + per_block - 1) / per_block), room = many && (waves == 8 || wide) ? 256 : 512;
     const double tile_us = many ? (wide ? 3.5 : !narrow ? 2.1 : waves == 8 ? 1.65 : 1.85) : (wide ? 3.0 : 2.1);      // measured, device full
     const double partials = (double)(a.tokens * a.q_heads * a.c.dim) * 8.0 / 4.0e6;
     int64_t splits = 1;
@@ -476,7 +497,7 @@ Plan plan_with(const KvAttnArgs& a, int waves) {
 // 9 x 6000, E4M3, 69 and 62; 256 of 16 x 8192 122 and 136, 8192 of 2 x 4096 190 and 202.
 Plan plan_of(const KvAttnArgs& a) {
     Plan best = plan_with(a, 0);
-    if (a.max_q * (a.q_heads / a.c.heads) <= (a.c.dim == 256 ? 16 : 32)) return best;
+    if (usual_q(a) * (a.q_heads / a.c.heads) <= (a.c.dim == 256 ? 16 : 32)) return best;
     for (int waves : {8, 4}) {
         if (a.c.dim != 64 && waves != (a.c.dim == 256 ? 4 : 8)) continue;
         const Plan p = plan_with(a, waves);
@@ -492,11 +513,13 @@ int64_t kv_attn_workspace(const KvAttnArgs& a) {
     return p.sp.splits > 1 ? (int64_t)p.sp.splits * a.tokens * a.q_heads * (a.c.dim + 1) * 4 : 0;
 }
 
-const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
-    const Plan p = plan_of(a);
+const char* launch_kv_attn(const KvAttnArgs& given, void* ws, hipStream_t s) {
+    const Plan p = plan_of(given);
+    KvAttnArgs a = given;
+    a.chunk = p.chunk;
     float* po = static_cast<float*>(ws);
     float* pl = po + (int64_t)p.sp.splits * a.tokens * a.q_heads * a.c.dim;
-    const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, (unsigned)a.batch);
+    const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, kv_grid_z(a));
     const char* name = nullptr;
     if (p.waves) name = launch_kv_attn_many(a, p.sp, p.row_blocks, p.waves, po, pl, s);
     else for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
@@ -505,10 +528,15 @@ const char* launch_kv_attn(const KvAttnArgs& a, void* ws, hipStream_t s) {
     });
     if (p.sp.splits > 1) {
         const bool wide = p.sp.splits > 8;
-        const dim3 join((unsigned)(wide ? a.max_q * a.q_heads : (a.max_q * a.q_heads + 3) / 4), (unsigned)a.batch);
+        const int64_t rows = (p.chunk ? p.chunk : a.max_q) * a.q_heads;
+        const dim3 join((unsigned)(wide ? rows : (rows + 3) / 4), (unsigned)a.batch);
         auto go = [&](auto D) {
-            if (wide) k_kv_attn_join<D(), 4><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
-            else k_kv_attn_join<D(), 1><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+            auto with = [&](auto TURNS) {
+                if (wide) k_kv_attn_join<D(), 4, TURNS()><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+                else k_kv_attn_join<D(), 1, TURNS()><<<join, 256, 0, s>>>(a, p.sp.splits, po, pl);
+            };
+            if (p.chunk) with(std::true_type{});
+            else with(std::false_type{});
         };
         if (a.c.dim == 64) go(std::integral_constant<int, 64>{});
         else if (a.c.dim == 128) go(std::integral_constant<int, 128>{});

@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
 
     const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = blockIdx.x % a.c.heads, split = blockIdx.y, b = blockIdx.z;
-    const int rb = gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads;     // the longest first
-    const KvSeq q = kv_seq(a, b);
-    const int G = a.q_heads / a.c.heads, rows = kv_rows(a, q), r0 = rb * WAVES * kRows;
-    if (r0 >= rows) return;
+    const int h = blockIdx.x % a.c.heads, split = blockIdx.y;
+    KvBlock own_rows;
+    if (!kv_block(a, gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads, WAVES * kRows, own_rows)) return;     // the longest first
+    const KvSeq q = own_rows.q;
+    const int G = a.q_heads / a.c.heads, rows = own_rows.rows, r0 = own_rows.r0, b = own_rows.b;
     const int last = (rows < r0 + WAVES * kRows ? rows : r0 + WAVES * kRows) - 1;
     const KvRange rg = kv_range<kT>(a, q, r0 / G, last / G);
     const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
 }  // namespace
 
 const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s) {
-    const dim3 grid((unsigned)a.c.heads * row_blocks, (unsigned)sp.splits, (unsigned)a.batch);
+    const dim3 grid((unsigned)a.c.heads * row_blocks, (unsigned)sp.splits, kv_grid_z(a));
     for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
         if constexpr (D() != 256) {
             if (waves == 8) k_kv_attn_many<FMT(), D(), 8><<<grid, 8 * 64, 0, s>>>(a, sp, po, pl);

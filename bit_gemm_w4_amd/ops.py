@@ -702,8 +702,8 @@ def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens:
     window only the last `window` of them and the first `sinks`.  A query that
     sees nothing gives zeros.  max_q_len and max_kv_len (0: the table's width)
     are host-side bounds of the lengths: a sequence's queries past max_q_len are
-    left alone, and without it (None) every sequence may own all T, which costs
-    speed with cu_q.  scale None: D ** -0.5.  lse: float32
+    left alone, and without it (None) every sequence may own all T, which with
+    cu_q costs some speed.  scale None: D ** -0.5.  lse: float32
     [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
     workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream
     (a captured graph: its own)."""

@@ -554,10 +554,11 @@ bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots, int64_t 
  * anything.
  *   q          element (t, h, i) at t * q_token_stride + h * q_head_stride + i;
  *              strides multiples of 8 elements
- *   cu_q       [batch + 1], or NULL: tokens == batch, one query each.  Entries
+ *   cu_q       [batch + 1], not decreasing, or NULL: tokens == batch, one query each.  Entries
  *              are clamped to 0..tokens; rows of out that no sequence owns are
  *              left alone.
- *   max_q      at least every sequence's query count (host value: sizes the grid;
+ *   max_q      at least every sequence's query count (host value: sizes the grid,
+ *              tokens if nothing is known, which costs some speed;
  *              the rows of out and lse of later queries are left alone)
  *   max_kv     at least every kv_lens entry, or 0 for the block table's width:
  *              sizes the split over positions; a smaller value costs only speed
