@@ -760,6 +760,125 @@ BG_EXPORT int64_t kv_attn_workspace_bytes(const bg_kv_attn* args) {
     return bg::kv_attn_workspace(a);
 }
 
+namespace {
+
+constexpr int64_t kMaxPoolPages = int64_t(1) << 30;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The pool of `fn`, checked.
+bg_status kv_pool_of(const char* fn, const bg_kv_pool* p, bg::KvPool* out) {
+    if (!p) return fail_in(fn, BG_ERR_NULL, "pool must be non-NULL");
+    if (!p->block_table || !p->lens || !p->free_pages || !p->state || (p->window && !p->gone))
+        return fail_in(fn, BG_ERR_NULL, "the pool's arrays must be non-NULL");
+    if (p->batch < 1 || p->batch > kMaxBatch) return fail_in(fn, BG_ERR_SHAPE, "batch=%lld out of range", p->batch);
+    if (p->page_size < 16 || p->page_size > 1024 || (p->page_size & (p->page_size - 1)))
+        return fail_in(fn, BG_ERR_SHAPE, "page_size %lld is not a power of two in 16..1024", p->page_size);
+    if (p->pages < 1 || p->pages > kMaxPoolPages) return fail_in(fn, BG_ERR_SHAPE, "pages=%lld out of range", p->pages);
+    const int shift = __builtin_ctz((unsigned)p->page_size);
+    if (p->max_pages < 1 || p->max_pages > ((INT32_MAX - 2 * kMaxTokens) >> shift))
+        return fail_in(fn, BG_ERR_SHAPE, "max_pages=%lld pages of %lld tokens are none, or pass 2^31 - 2^25 positions", p->max_pages, p->page_size);
+    if (p->window < 0 || p->sinks < 0) return fail_in(fn, BG_ERR_SHAPE, "window=%lld and sinks=%lld must not be negative", p->window, p->sinks);
+    if (!aligned(p->block_table, 4) || !aligned(p->lens, 4) || !aligned(p->gone, 4) || !aligned(p->free_pages, 4) || !aligned(p->state, 4))
+        return fail_in(fn, BG_ERR_ALIGN, "the pool's arrays must be 4-byte aligned");
+    auto clamped = [](int64_t n) { return (int)(n > INT32_MAX ? INT32_MAX : n); };
+    *out = bg::KvPool{p->block_table, p->lens, p->gone, p->free_pages, p->state, p->batch, p->max_pages, p->pages,
+                      shift, clamped(p->window), clamped(p->sinks)};
+    return BG_OK;
+}
+
+// The rows of `fn`, checked; kv_heads and dim: the cache's, or the arguments' own (0).
+bg_status rope_args(const char* fn, const bg_qk_rope* p, const bg::KvCache* cache, bg::RopeArgs* a, int* dim) {
+    if (!p) return fail_in(fn, BG_ERR_NULL, "args must be non-NULL");
+    const int kv_heads = cache ? cache->heads : p->kv_heads;
+    *dim = cache ? cache->dim : p->head_dim;
+    if (p->x_dtype != BG_F32 && p->x_dtype != BG_F16 && p->x_dtype != BG_BF16)
+        return fail_in(fn, BG_ERR_DTYPE, "x_dtype %lld is not F32/F16/BF16", p->x_dtype);
+    if ((p->q_weight || p->k_weight) && p->weight_dtype != p->x_dtype && p->weight_dtype != BG_F32)
+        return fail_in(fn, BG_ERR_DTYPE, "weight_dtype %lld is neither x_dtype nor F32", p->weight_dtype);
+    if (*dim != 64 && *dim != 128 && *dim != 256) return fail_in(fn, BG_ERR_SHAPE, "head_dim %lld is not 64, 128 or 256", *dim);
+    if (p->rot < 0 || p->rot > *dim || p->rot % 8)
+        return fail_in(fn, BG_ERR_SHAPE, "rot=%lld is not a multiple of 8 up to head_dim=%lld", p->rot, *dim);
+    if (p->q_heads < 0 || p->q_heads > 16384 || kv_heads < 0 || kv_heads > 16384 || p->q_heads + kv_heads == 0)
+        return fail_in(fn, BG_ERR_SHAPE, "q_heads=%lld, kv_heads=%lld out of range", p->q_heads, kv_heads);
+    if (p->tokens < 0 || p->tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", p->tokens);
+    const int64_t heads = p->q_heads > kv_heads ? p->q_heads : kv_heads;
+    if (p->tokens * heads > (int64_t(1) << 28)) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld times %lld heads pass 2^28", p->tokens, heads);
+    if (!(p->eps >= 0.0) || p->eps > 1.0e30 || !(p->weight_offset >= -1.0e30 && p->weight_offset <= 1.0e30))
+        return fail_in(fn, BG_ERR_SHAPE, "eps must be at least 0, eps and weight_offset finite");
+    const int64_t unit = p->x_dtype == BG_F32 ? 4 : 8;   // elements in 16 bytes
+    const bool q = p->q_heads > 0, k = kv_heads > 0, k_out = k && !cache;
+    if ((q && (p->q_token_stride % unit || p->q_head_stride % unit || p->q_out_token_stride % unit || p->q_out_head_stride % unit)) ||
+        (k && (p->k_token_stride % unit || p->k_head_stride % unit)) || (k_out && (p->k_out_token_stride % unit || p->k_out_head_stride % unit)) ||
+        (cache && (p->v_token_stride % unit || p->v_head_stride % unit)))
+        return fail_in(fn, BG_ERR_ALIGN, "strides must be multiples of 16 bytes (%lld elements)", unit);
+    if (p->tokens > 0) {
+        if ((q && (!p->q || !p->q_out)) || (k && !p->k) || (k_out && !p->k_out) || (cache && (!p->v || !p->slots)))
+            return fail_in(fn, BG_ERR_NULL, "the rows of queries and keys, their outputs, v and slots must be non-NULL");
+        if (p->rot && (!p->positions || !p->freqs)) return fail_in(fn, BG_ERR_NULL, "positions and freqs must be non-NULL");
+        if ((q && (!aligned16(p->q) || !aligned16(p->q_out))) || (k && !aligned16(p->k)) || (k_out && !aligned16(p->k_out)) ||
+            (cache && !aligned16(p->v)) || !aligned16(p->q_weight) || !aligned16(p->k_weight))
+            return fail_in(fn, BG_ERR_ALIGN, "rows and weights must be 16-byte aligned");
+        if ((p->rot && (!aligned(p->positions, 4) || !aligned(p->freqs, 8))) || (cache && !aligned(p->slots, 8)))
+            return fail_in(fn, BG_ERR_ALIGN, "positions must be 4-byte aligned, freqs and slots 8-byte aligned");
+    }
+    *a = bg::RopeArgs{p->q, p->k, p->v, p->q_out, p->k_out, p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
+                      p->v_token_stride, p->v_head_stride, p->q_out_token_stride, p->q_out_head_stride, p->k_out_token_stride,
+                      p->k_out_head_stride, p->q_weight, p->k_weight, p->positions, p->freqs, p->slots, p->tokens, p->q_heads, kv_heads,
+                      p->rot, p->interleaved != 0, p->weight_dtype == BG_F32, p->eps, p->weight_offset};
+    return BG_OK;
+}
+
+bg_status rope_impl(const char* fn, const bg_qk_rope* args, const bg::KvCache* cache, void* stream) {
+    bg::RopeArgs a;
+    int dim = 0;
+    const bg_status st = rope_args(fn, args, cache, &a, &dim);
+    if (st != BG_OK) return st;
+    if (a.tokens == 0) {
+        g_last_error[0] = '\0';
+        return BG_OK;
+    }
+    note_kernel(bg::launch_qk_rope(a, args->x_dtype, dim, cache, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+}  // namespace
+
+BG_EXPORT bg_status kv_plan(const bg_kv_pool* pool, const int32_t* q_lens, int64_t tokens, int advance, int32_t* cu_q,
+                            int32_t* kv_lens, int32_t* served, int32_t* positions, int64_t* slots, void* stream) {
+    const char* fn = "kv_plan";
+    bg::KvPool p;
+    const bg_status st = kv_pool_of(fn, pool, &p);
+    if (st != BG_OK) return st;
+    if (tokens < 0 || tokens > kMaxTokens) return fail_in(fn, BG_ERR_SHAPE, "tokens=%lld out of range", tokens);
+    if (!q_lens || !cu_q || !kv_lens || !served || (tokens > 0 && (!positions || !slots)))
+        return fail_in(fn, BG_ERR_NULL, "q_lens, cu_q, kv_lens, served, positions and slots must be non-NULL");
+    if (!aligned(q_lens, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(served, 4) || !aligned(positions, 4) || !aligned(slots, 8))
+        return fail_in(fn, BG_ERR_ALIGN, "lengths, offsets and positions must be 4-byte aligned, slots 8-byte aligned");
+    const bg::KvPlan o{q_lens, tokens, advance != 0, cu_q, kv_lens, served, positions, slots};
+    note_kernel(bg::launch_kv_plan(p, o, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+BG_EXPORT bg_status kv_release(const bg_kv_pool* pool, const int32_t* keep, void* stream) {
+    const char* fn = "kv_release";
+    bg::KvPool p;
+    const bg_status st = kv_pool_of(fn, pool, &p);
+    if (st != BG_OK) return st;
+    if (!aligned(keep, 4)) return fail_in(fn, BG_ERR_ALIGN, "keep must be 4-byte aligned");
+    note_kernel(bg::launch_kv_release(p, keep, static_cast<hipStream_t>(stream)));
+    return launched(fn);
+}
+
+BG_EXPORT bg_status qk_norm_rope(const bg_qk_rope* args, void* stream) { return rope_impl("qk_norm_rope", args, nullptr, stream); }
+
+BG_EXPORT bg_status kv_cache_write_rope(const bg_kv_cache* cache, const bg_qk_rope* args, void* stream) {
+    const char* fn = "kv_cache_write_rope";
+    bg::KvCache c;
+    const bg_status st = kv_cache_of(fn, cache, &c);
+    return st == BG_OK ? rope_impl(fn, args, &c, stream) : st;
+}
+
 BG_EXPORT const char* bg_status_string(int status) {
     switch (status) {
         case BG_OK: return "ok";

@@ -12,6 +12,7 @@ import ctypes
 import os
 import struct
 from dataclasses import dataclass
+from fractions import Fraction
 
 import torch
 
@@ -31,6 +32,7 @@ EXPORTS = (
     "gemm_w8a8_ex", "gemm_w8a8_ws", "gemm_w8a8_workspace_bytes", "gemm_w4a8", "gemm_w4a8_ws", "gemm_w4a8_workspace_bytes",
     "gemm_w4a16_algo", "gemm_w8a8_algo",
     "kv_cache_write", "kv_cache_read", "kv_attn", "kv_attn_tree", "kv_attn_workspace_bytes",
+    "kv_plan", "kv_release", "qk_norm_rope", "kv_cache_write_rope",
     "bg_status_string", "bg_last_error",
     "bg_pack_format_version", "bg_last_kernel",
 )
@@ -89,6 +91,10 @@ def lib() -> ctypes.CDLL:
             "kv_attn": [P, P, I64, P],
             "kv_attn_tree": [P, P, I64, P],
             "kv_attn_workspace_bytes": [P],
+            "kv_plan": [P, P, I64, I, P, P, P, P, P, P],
+            "kv_release": [P, P, P],
+            "qk_norm_rope": [P, P],
+            "kv_cache_write_rope": [P, P, P],
             "bg_status_string": [I],
             "bg_last_error": [],
             "bg_pack_format_version": [],
@@ -544,12 +550,15 @@ def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, format: i
     return KVCache(*codes, *scales, format)
 
 
-def _on_device(fn: str, cache: KVCache, *tensors):
+def _on_device(fn: str, owner, *tensors):
+    """owner: the cache, the pool or the rows whose device the call runs on."""
     for t in tensors:
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{fn}: operands must be on the cache's device {cache.device}, got {t.device}")
-    if cache.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: the cache is on {cache.device}, the current device is {torch.cuda.current_device()}")
+        if t is not None and t.device != owner.device:
+            raise ValueError(f"{fn}: operands must be on one device, {owner.device}, got {t.device}")
+    if owner.device.type != "cuda":
+        raise ValueError(f"{fn}: operands must be device tensors")
+    if owner.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the operands are on {owner.device}, the current device is {torch.cuda.current_device()}")
 
 
 def _raw_stream(device: int) -> int:
@@ -741,3 +750,247 @@ def kv_attn_workspace_bytes(q_shape, cache: KVCache, batch: int, max_pages: int,
     return int(lib().kv_attn_workspace_bytes(_KV_ATTN.pack(
         cache.address, 0, 0, 0, 0, max_pages, 0, 256, 0, 0, 0, q_shape[0], batch, max_q_len, max_kv_len, window, sinks,
         q_shape[1], BF16, tree_words, 1.0)))
+
+
+# ------------------------------------------- pages of a cache, steps ---------
+
+_KV_POOL = struct.Struct("@PPPPPqqqqqi4x")            # bg_kv_pool
+
+
+def _int32(fn: str, t: torch.Tensor, shape: tuple, name: str) -> None:
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+@dataclass(frozen=True)
+class KVPool:
+    """The pages of a cache, those that sequences hold and those that are free, on
+    the device: block_table int32 [batch][pages of a sequence] and lens int32
+    [batch] (what kv_attn takes), gone int32 [batch] (with a window: pages from the
+    sinks' to this one were given back), free int32 [pages], of which the first
+    state[0] are free (a stack), and state int32 [2], whose second word is 0.
+    window and sinks: those of the attention that reads the cache (kv_release)."""
+    block_table: torch.Tensor
+    lens: torch.Tensor
+    gone: torch.Tensor
+    free: torch.Tensor
+    state: torch.Tensor
+    page_size: int
+    window: int = 0
+    sinks: int = 0
+
+    def __post_init__(self):
+        fn = "KVPool"
+        if self.block_table.dim() != 2 or self.free.dim() != 1:
+            raise ValueError(f"{fn}: block_table must be a matrix and free a vector")
+        batch, max_pages = self.block_table.shape
+        for t, shape, name in ((self.block_table, (batch, max_pages), "block_table"), (self.lens, (batch,), "lens"), (self.gone, (batch,), "gone"),
+                               (self.free, tuple(self.free.shape), "free"), (self.state, (2,), "state")):
+            _int32(fn, t, shape, name)
+        tensors = (self.block_table, self.lens, self.gone, self.free, self.state)
+        if any(t.device != self.lens.device for t in tensors):
+            raise ValueError(f"{fn}: the tensors must be on one device")
+        if batch < 1 or max_pages < 1 or self.free.shape[0] < 1:
+            raise ValueError(f"{fn}: a pool has at least one sequence, one page of it and one page")
+        if self.page_size < 16 or self.page_size > 1024 or self.page_size & (self.page_size - 1):
+            raise ValueError(f"{fn}: page_size {self.page_size} must be a power of two in 16..1024")
+        if self.window < 0 or self.sinks < 0:
+            raise ValueError(f"{fn}: window and sinks must not be negative")
+        ptrs = [_ptr(t).value for t in tensors]
+        desc = ctypes.create_string_buffer(_KV_POOL.pack(*ptrs, batch, max_pages, self.free.shape[0], self.window, self.sinks, self.page_size),
+                                           _KV_POOL.size)
+        for name, value in (("_desc", desc), ("address", ctypes.addressof(desc)), ("device", self.lens.device), ("batch", batch)):
+            object.__setattr__(self, name, value)
+
+    # Copies and pickles carry the fields alone: the descriptor of the new tensors is their own.
+    def __getstate__(self):
+        return self.block_table, self.lens, self.gone, self.free, self.state, self.page_size, self.window, self.sinks
+
+    def __setstate__(self, state):
+        for name, value in zip(("block_table", "lens", "gone", "free", "state", "page_size", "window", "sinks"), state):
+            object.__setattr__(self, name, value)
+        self.__post_init__()
+
+    @property
+    def _tensors(self):
+        return self.block_table, self.lens, self.gone, self.free, self.state
+
+
+def kv_pool(pages: int, page_size: int, batch: int, max_pages: int, *, window: int = 0, sinks: int = 0, device="cuda") -> KVPool:
+    """A pool of `pages` free pages for `batch` sequences that hold nothing, of up to max_pages pages each."""
+    zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+    state = zeros(2)
+    state[0] = pages
+    return KVPool(zeros(batch, max_pages) - 1, zeros(batch), zeros(batch), torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device), state,
+                  page_size, window, sinks)
+
+
+@dataclass(frozen=True)
+class KVPlan:
+    """A planned step (kv_plan): cu_q int32 [batch + 1], kv_lens, served int32
+    [batch], positions int32 and slots int64 [tokens]."""
+    cu_q: torch.Tensor
+    kv_lens: torch.Tensor
+    served: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+
+
+def kv_plan(pool: KVPool, q_lens: torch.Tensor, tokens: int, *, advance: bool = True, out: KVPlan | None = None, stream=None) -> KVPlan:
+    """Plan a step in which sequence b gets q_lens[b] (int32 [batch], on the
+    device) new tokens, its rows of the step's `tokens`: what kv_cache_write and
+    kv_attn take of it (slots; cu_q and kv_lens), and the rows' positions.  The
+    pool's block table gets the new pages, off the stack of free ones.  A sequence
+    that does not fit (its rows pass `tokens`, its length the block table, or the
+    free pages are used up by it and those before it) is not served: its length
+    stays, its rows' slots are -1, and served[b] is 0.  Rows past the last sequence's have slot -1
+    and position 0.  advance False: the pool's lengths and free pages stay as they
+    are, as for drafts that are yet to be accepted.  out: an earlier plan
+    of the same sizes, to be written over."""
+    fn = "kv_plan"
+    if stream is not None:
+        used = () if out is None else (out.cu_q, out.kv_lens, out.served, out.positions, out.slots)
+        return _on_stream(stream, (q_lens, *pool._tensors, *used), lambda: kv_plan(pool, q_lens, tokens, advance=advance, out=out))
+    B = pool.batch
+    _int32(fn, q_lens, (B,), "q_lens")
+    if out is None:
+        if tokens < 0:
+            raise ValueError(f"{fn}: tokens={tokens} is negative")
+        ints = torch.empty(3 * B + 1 + tokens, dtype=torch.int32, device=pool.device)
+        out = KVPlan(ints[:B + 1], ints[B + 1:2 * B + 1], ints[2 * B + 1:3 * B + 1], ints[3 * B + 1:],
+                     torch.empty(tokens, dtype=torch.int64, device=pool.device))
+    else:
+        for t, n, name in ((out.cu_q, B + 1, "cu_q"), (out.kv_lens, B, "kv_lens"), (out.served, B, "served"), (out.positions, tokens, "positions")):
+            _int32(fn, t, (n,), f"out.{name}")
+        if _kv_slots(fn, out.slots) != tokens:
+            raise ValueError(f"{fn}: out.slots must have {tokens} entries")
+    _on_device(fn, pool, q_lens, out.cu_q, out.kv_lens, out.served, out.positions, out.slots)
+    _check(lib().kv_plan(pool.address, q_lens.data_ptr(), tokens, advance, out.cu_q.data_ptr(), out.kv_lens.data_ptr(), out.served.data_ptr(),
+                         out.positions.data_ptr(), out.slots.data_ptr(), _raw_stream(pool.device.index)), fn)
+    return out
+
+
+def kv_release(pool: KVPool, keep: torch.Tensor | None = None, stream=None) -> None:
+    """Leave sequence b its first keep[b] tokens (int32 [batch]; None: all; 0: it
+    has ended) and give back its other pages; with the pool's window those too that
+    no query from its next position on sees.  A step taken back leaves the
+    stack of free pages as it was."""
+    fn = "kv_release"
+    if stream is not None:
+        return _on_stream(stream, (keep, *pool._tensors), lambda: kv_release(pool, keep))
+    if keep is not None:
+        _int32(fn, keep, (pool.batch,), "keep")
+    _on_device(fn, pool, keep)
+    _check(lib().kv_release(pool.address, None if keep is None else keep.data_ptr(), _raw_stream(pool.device.index)), fn)
+
+
+# ------------------------------------- norms and rotation of heads -----------
+
+_QK_ROPE = struct.Struct("@PPPPPqqqqqqqqqqPPPPPqddiiiiiii4x")     # bg_qk_rope
+_PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923, 10 ** 64)
+
+
+def rope_freqs(inv_freq) -> torch.Tensor:
+    """Frequencies in radians a position (rot / 2 of them, a tensor or a list; a
+    float's value counts as it is) as the turns in units of 2^-64 that qk_norm_rope
+    takes: int64 [rot / 2], on the tensor's device.  Made once: it reads the tensor on the host."""
+    values = inv_freq.detach().double().flatten().tolist() if isinstance(inv_freq, torch.Tensor) else [float(x) for x in inv_freq]
+    turns = [round(Fraction(x) * 2 ** 63 / _PI) % 2 ** 64 for x in values]
+    out = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64)
+    return out.to(inv_freq.device) if isinstance(inv_freq, torch.Tensor) else out
+
+
+def _rope_rows(fn: str, t: torch.Tensor, name: str, tokens: int, dt, dim: int) -> tuple:
+    """The token and head strides of rows [tokens][heads][dim]."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or t.dtype != dt or t.stride(2) != 1:
+        raise ValueError(f"{fn}: {name} must be [{tokens}][heads][{dim}] of {dt} with a contiguous last axis, got {t.dtype} {tuple(t.shape)}")
+    return 0 if tokens == 1 else t.stride(0), 0 if t.shape[1] == 1 else t.stride(1)      # an axis of one element may have any stride
+
+
+def _qk_rope(fn, q, k, v, cache, slots, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, k_out):
+    x = q if k is None else k
+    if x is None:
+        raise ValueError(f"{fn}: queries or keys must be given")
+    if x.dim() != 3:
+        raise ValueError(f"{fn}: rows must be [tokens][heads][D], got {tuple(x.shape)}")
+    T, dim = x.shape[0], x.shape[2]
+    dt = _TORCH_DT.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"{fn}: rows must be float32, float16 or bfloat16, got {x.dtype}")
+    strides, ptrs, outs = [], [], []
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        strides += (0, 0) if t is None else _rope_rows(fn, t, name, T, x.dtype, dim)
+        ptrs.append(0 if t is None else t.data_ptr())
+    for t, given, name in ((q, q_out, "q_out"), (None if cache is not None else k, k_out, "k_out")):
+        if t is None:
+            if given is not None:
+                raise ValueError(f"{fn}: {name} without its rows")
+            outs.append(None)
+            strides += (0, 0)
+            ptrs.append(0)
+            continue
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device) if given is None else given
+        if out.shape != t.shape:
+            raise ValueError(f"{fn}: {name} must be {tuple(t.shape)}, got {tuple(out.shape)}")
+        strides += _rope_rows(fn, out, name, T, x.dtype, dim)
+        ptrs.append(out.data_ptr())
+        outs.append(out)
+    rot = 0
+    if freqs is not None:
+        if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise ValueError(f"{fn}: freqs must be a contiguous int64 vector (rope_freqs)")
+        rot = 2 * freqs.shape[0]
+        if positions is None:
+            raise ValueError(f"{fn}: positions must be given")
+    if positions is not None:
+        _int32(fn, positions, (T,), "positions")
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w in weights:
+        if w.dtype not in (x.dtype, torch.float32) or w.dtype != weights[0].dtype or tuple(w.shape) != (dim,) or not w.is_contiguous():
+            raise ValueError(f"{fn}: weights must be contiguous vectors of {dim}, both of {x.dtype} or both float32")
+    _on_device(fn, x if cache is None else cache, q, k, v, *outs, slots, positions, freqs, *weights)
+    if T == 0:
+        return outs
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    args = _QK_ROPE.pack(*ptrs, *strides, ptr(q_weight), ptr(k_weight), ptr(positions), ptr(freqs), ptr(slots), T, eps, weight_offset,
+                         0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim, rot, interleaved, dt,
+                         _TORCH_DT[weights[0].dtype] if weights else dt)
+    s = _raw_stream(x.device.index)
+    _check(lib().qk_norm_rope(args, s) if cache is None else lib().kv_cache_write_rope(cache.address, args, s), fn)
+    return outs
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None, freqs: torch.Tensor | None, *,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                 interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm each head of queries [T][q_heads][D] and keys [T][kv_heads][D] (either
+    may be None) and rotate it by its position (int32 [T]) -> (q, k), new tensors
+    unless q_out / k_out are given (the rows themselves for in place).
+
+    x / sqrt(mean(x^2) + eps) * (weight_offset + weight), where a weight [D] is
+    given; then the first 2 len(freqs) elements in pairs (n, n + len(freqs)), or with interleaved
+    (2 n, 2 n + 1), by the angle position * frequency n (freqs: rope_freqs; None: no
+    rotation).  Rows may be slices of a fused projection's, as in kv_cache_write."""
+    if stream is not None:
+        return _on_stream(stream, (q, k, positions, freqs, q_weight, k_weight, q_out, k_out),
+                          lambda: qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight, eps=eps, weight_offset=weight_offset,
+                                               interleaved=interleaved, q_out=q_out, k_out=k_out))
+    return tuple(_qk_rope("qk_norm_rope", q, k, None, None, None, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, k_out))
+
+
+def kv_cache_write_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Tensor, positions: torch.Tensor | None,
+                        freqs: torch.Tensor | None, *, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                        eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor | None:
+    """qk_norm_rope and kv_cache_write in one pass: queries are normed and rotated
+    (-> new tensor, or q_out; None: none), keys too, and go to the cache slots with the values.
+    Keys are computed in float64 and rounded to float32, from which they are quantized."""
+    if stream is not None:
+        return _on_stream(stream, (q, k, v, cache.k, cache.v, cache.k_scales, cache.v_scales, slots, positions, freqs, q_weight, k_weight, q_out),
+                          lambda: kv_cache_write_rope(q, k, v, cache, slots, positions, freqs, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                                      weight_offset=weight_offset, interleaved=interleaved, q_out=q_out))
+    fn = "kv_cache_write_rope"
+    shape = (_kv_slots(fn, slots), cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"{fn}: k {tuple(k.shape)} and v {tuple(v.shape)} must be {shape}")
+    return _qk_rope(fn, q, k, v, cache, slots, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, None)[0]

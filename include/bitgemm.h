@@ -602,6 +602,122 @@ bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspac
  * sizes only: apart from cache and cu_q (NULL or not), pointers may be NULL. */
 int64_t kv_attn_workspace_bytes(const bg_kv_attn* args);
 
+/*
+ * A pool of a cache's pages: the block table of `batch` sequences, the tokens
+ * that each holds, and the pages that none holds.  The caller allocates the
+ * arrays; an empty pool has lens, gone and state[1] 0, state[0] = pages and
+ * free_pages a list of all pages.
+ *   block_table  [batch][max_pages]; a sequence's entries from ceil(lens / page_size)
+ *                on mean nothing
+ *   lens         [batch] tokens held (clamped to 0 .. max_pages * page_size)
+ *   gone         [batch], with a window: the sequence's pages from its sinks' to
+ *                this one were given back
+ *   free_pages   [pages], a stack: the first state[0] are free
+ *   state        [2]: the number of free pages, and a word that is 0 between calls
+ *   window, sinks  as in kv_attn: what the calls that read the cache see of it
+ * Calls on one pool must not overlap in time.
+ */
+typedef struct bg_kv_pool {
+    int32_t* block_table;
+    int32_t* lens;
+    int32_t* gone;
+    int32_t* free_pages;
+    int32_t* state;
+    int64_t batch;
+    int64_t max_pages;
+    int64_t pages;
+    int64_t window;
+    int64_t sinks;
+    int32_t page_size;
+} bg_kv_pool;
+
+/*
+ * kv_plan -- a step in which sequence b gets q_lens[b] new tokens (0 or less:
+ * none): rows cu_q[b] .. cu_q[b + 1] - 1 of the step, at its positions lens[b]
+ * and up.  New pages come off the stack in the order of the sequences, a
+ * sequence's pages in their order.  A sequence is served if its rows lie within
+ * `tokens`, its positions within the block table, and it needs no page or the
+ * pages that it and those before it need (such as have the first two) are there;
+ * one that is not gets none, its tokens have no slots and its length stays.
+ *   cu_q       out [batch + 1], clamped to tokens
+ *   kv_lens    out [batch]: the lengths with the new tokens
+ *   served     out [batch]: 1 or 0
+ *   positions  out [tokens]: of each row (of rows past the last sequence's: 0)
+ *   slots      out [tokens]: where the row's token goes, -1: nowhere
+ * The block table gets the new pages.  advance != 0: the pool holds the new
+ * tokens from now on; 0: lengths and free pages stay, and the entries of the new
+ * pages mean nothing after the step (drafts that are yet to be accepted).
+ */
+bg_status kv_plan(const bg_kv_pool* pool, const int32_t* q_lens, int64_t tokens, int advance, int32_t* cu_q,
+                  int32_t* kv_lens, int32_t* served, int32_t* positions, int64_t* slots, void* stream);
+
+/*
+ * kv_release -- leaves sequence b its first keep[b] tokens (keep NULL: all; 0 or
+ * less: none, the sequence has ended) and puts the other pages back on the
+ * stack; with a window those too that no query at its next position or later sees
+ * (keep must not lie in what was given back so before: such positions stay gone).
+ * The order is that of kv_plan backwards: a step taken back leaves the stack as
+ * it was.  Their block table entries become -1.
+ */
+bg_status kv_release(const bg_kv_pool* pool, const int32_t* keep, void* stream);
+
+/*
+ * qk_norm_rope -- norms of each head of queries and keys, and the rotation of
+ * their first `rot` elements by their positions:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)   (weight NULL: y = x)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = position * frequency n
+ * for the pairs n of elements (n, rot / 2 + n), or (2 n, 2 n + 1) if interleaved.
+ *   q, k       element (t, h, i) at t * token_stride + h * head_stride + i, of
+ *              x_dtype (F32, F16 or BF16); strides in elements, multiples of 16 bytes.
+ *              Either has no heads (q_heads or kv_heads 0) where it is not wanted
+ *   q_out, k_out  the same with strides of their own; may be q and k (then with
+ *              their strides), and overlap no other input
+ *   q_weight, k_weight  [head_dim] of weight_dtype (x_dtype or F32), or NULL
+ *   positions  [tokens], any values
+ *   freqs      [rot / 2] turns (of 2 pi) a position in units of 2^-64, so that
+ *              position * freqs[n] mod 2^64 is the angle's fraction of a turn
+ * Requires head_dim 64, 128 or 256, rot a multiple of 8 from 0 to head_dim (0: no
+ * rotation; freqs may be NULL), tokens times either's heads at most 2^28.
+ * Computed in binary32 (angles exactly), rounded once to x_dtype.  tokens = 0
+ * enqueues nothing.
+ *
+ * kv_cache_write_rope -- the same for queries; keys are computed in binary64,
+ * rounded to binary32 and go to the cache with the values, as kv_cache_write
+ * quantizes them.  kv_heads and head_dim are the cache's, k_out is not used.
+ *   v          as k, without norm and rotation
+ *   slots      as in kv_cache_write
+ */
+typedef struct bg_qk_rope {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride;
+    int64_t k_out_token_stride, k_out_head_stride;
+    const void* q_weight;
+    const void* k_weight;
+    const int32_t* positions;
+    const uint64_t* freqs;
+    const int64_t* slots;
+    int64_t tokens;
+    double eps;
+    double weight_offset;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t rot;
+    int32_t interleaved;
+    int32_t x_dtype;
+    int32_t weight_dtype;
+} bg_qk_rope;
+
+bg_status qk_norm_rope(const bg_qk_rope* args, void* stream);
+bg_status kv_cache_write_rope(const bg_kv_cache* cache, const bg_qk_rope* args, void* stream);
+
 /* Static description of a status code. */
 const char* bg_status_string(int status);
 /* Message of the last failed call on this host thread ("" if none). */
