@@ -78,6 +78,10 @@ struct KvAttnArgs {
     float scale;
     void* out;                 // [tokens][q_heads][D]
     float* lse;                // [tokens][q_heads], or NULL
+    bool scored;               // any of the following
+    float cap, cap_inv;        // scores are capped: cap tanh(score cap_inv), in base-2 units; 0: not
+    const float* slopes;       // [q_heads]: less slope times distance; or NULL
+    const int32_t* prefix;     // [batch]: positions below it are seen from before, too; or NULL
 };
 
 // The pages of a cache that sequences do not hold, and those that they do.

@@ -16,11 +16,13 @@ struct KvSplit {
 
 // A sequence: its queries are rows q0 .. q0 + len - 1 of q and stand at
 // positions first .. first + len - 1 = kv - 1.
+// Each query sees positions below `prefix` whatever its own (SCORED; else 0).
 struct KvSeq {
     int64_t q0;
-    int len, kv, first;
+    int len, kv, first, prefix;
 };
 
+template <bool SCORED>
 __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
     KvSeq q;
     int64_t q0 = b, q1 = b + 1;
@@ -35,6 +37,13 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
     q.kv = (int)(kv < 0 ? 0 : kv > room ? room : kv);
     q.len = (int)(q1 - q0);
     q.first = q.kv - q.len;
+    q.prefix = 0;
+    if constexpr (SCORED) {
+        if (a.prefix) {
+            const int n = a.prefix[b];
+            q.prefix = n < 0 ? 0 : n > q.kv ? q.kv : n;
+        }
+    }
     return q;
 }
 
@@ -53,11 +62,12 @@ struct KvBlock {
 // the batch, of those queries from `chunk` on whose sequence holds token (z - batch) chunk,
 // up to the next such token.  Between two such tokens no sequence has queries from `chunk`
 // on but the one that holds the first.  False: none.
+template <bool SCORED>
 __device__ __forceinline__ bool kv_block(const KvAttnArgs& a, int rb, int per_block, KvBlock& o) {
     const int G = a.q_heads / a.c.heads, z = blockIdx.z;
     if (z < (int)a.batch) {
         o.b = z;
-        o.q = kv_seq(a, z);
+        o.q = kv_seq<SCORED>(a, z);
         o.rows = kv_rows(a, o.q);
         if (a.chunk && o.rows > (int)a.chunk * G) o.rows = (int)a.chunk * G;
         o.r0 = rb * per_block;
@@ -70,7 +80,7 @@ __device__ __forceinline__ bool kv_block(const KvAttnArgs& a, int rb, int per_bl
             else high = mid - 1;
         }
         o.b = low;
-        o.q = kv_seq(a, low);
+        o.q = kv_seq<SCORED>(a, low);
         const int64_t at = t - o.q.q0;
         if (at < 0 || at >= o.q.len) return false;
         const int64_t first = at < a.chunk ? a.chunk : at, end = at + a.chunk < o.q.len ? at + a.chunk : o.q.len;
@@ -81,6 +91,7 @@ __device__ __forceinline__ bool kv_block(const KvAttnArgs& a, int rb, int per_bl
 }
 
 // Whether query i of the sequence sees position j < kv (its page aside).
+template <bool SCORED>
 __device__ __forceinline__ bool kv_sees(const KvAttnArgs& a, const KvSeq& q, int i, int j) {
     if (a.tree) {
         const int e = j - q.first;
@@ -88,7 +99,7 @@ __device__ __forceinline__ bool kv_sees(const KvAttnArgs& a, const KvSeq& q, int
         return j < q.kv && e < 64 * a.tree_words && (a.tree[(q.q0 + i) * a.tree_words + (e >> 6)] >> (e & 63) & 1);
     }
     const int at = q.first + i;
-    return j <= at && (a.window == 0 || j > at - (int)a.window || j < (int)a.sinks);
+    return (j <= at || (SCORED && j < q.prefix)) && (a.window == 0 || j > at - (int)a.window || j < (int)a.sinks);
 }
 
 // What queries i0 .. i1 see between them: positions [0, sink) and [low, high),
@@ -106,7 +117,7 @@ struct KvRange {
     __device__ __forceinline__ int tile(int n) const { return n < sink_tiles ? n : n - sink_tiles + low_tile; }
 };
 
-template <int T>
+template <int T, bool SCORED>
 __device__ __forceinline__ KvRange kv_range(const KvAttnArgs& a, const KvSeq& q, int i0, int i1) {
     KvRange r;
     if (a.tree) {
@@ -117,6 +128,10 @@ __device__ __forceinline__ KvRange kv_range(const KvAttnArgs& a, const KvSeq& q,
         const int at0 = q.first + i0, at1 = q.first + i1;
         r.high = at1 + 1 > 0 ? at1 + 1 : 0;
         r.all_high = at0 + 1;
+        if constexpr (SCORED) {
+            r.high = r.high > q.prefix ? r.high : q.prefix;
+            r.all_high = r.all_high > q.prefix ? r.all_high : q.prefix;
+        }
         const int w = (int)a.window;
         r.low = w && at0 - w + 1 > 0 ? at0 - w + 1 : 0;
         r.all_low = w && at1 - w + 1 > 0 ? at1 - w + 1 : 0;
@@ -227,6 +242,37 @@ __device__ __forceinline__ RowStep raise_row(float& m, float& fb, float ty, floa
     m = m1;
     fb = __uint_as_float((uint32_t)(127 - (int)b) << 23);
     return f;
+}
+
+// Scores t (base 2) to cap tanh(t / cap).  Where no lane's |u| = |t| / cap passes 1, as usually
+// with the caps in use, tanh(u) / u is a polynomial in u^2 (a minimax fit, off by 2^-24):
+// 9 vector instructions a score; beyond, 1 - 2 / (1 + e^2|u|) beside it, whose two
+// transcendentals cost as much as 8 others.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&t)[N], float cap, float inv) {
+    float u[N], top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        u[j] = t[j] * inv;
+        top = __builtin_fmaxf(top, __builtin_fabsf(u[j]));
+        const float z = u[j] * u[j];
+        float p = 0x1.10e5d6p-10f;
+        p = __builtin_fmaf(p, z, -0x1.968b6cp-8f);
+        p = __builtin_fmaf(p, z, 0x1.4c6e58p-6f);
+        p = __builtin_fmaf(p, z, -0x1.b5eb84p-5f);
+        p = __builtin_fmaf(p, z, 0x1.10e672p-3f);
+        p = __builtin_fmaf(p, z, -0x1.55540ap-2f);
+        p = __builtin_fmaf(p, z, 0x1.fffffep-1f);
+        t[j] *= p;
+    }
+    if (__any(top > 1.0f)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(u[j]) * 0x1.715476p1f);
+            const float y = cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+            t[j] = __builtin_fabsf(u[j]) > 1.0f ? __builtin_copysignf(y, u[j]) : t[j];
+        }
+    }
 }
 
 // Two small unsigned integers in the halves of w, read as FP16 subnormals

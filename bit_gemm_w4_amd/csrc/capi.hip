@@ -36,6 +36,7 @@ bg_status fail_in(const char* fn, bg_status st, const char* fmt, long long a = 0
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 bg_status launched(const char* what) {
     const hipError_t e = hipGetLastError();
@@ -682,9 +683,23 @@ bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool poin
     return BG_OK;
 }
 
-bg_status kv_attn_impl(const char* fn, const bg_kv_attn* p, bool tree, void* ws, int64_t ws_bytes, void* stream) {
+// What `sc` asks of the scores, checked.
+bg_status kv_scores(const char* fn, const bg_kv_scores* sc, bool tree, bg::KvAttnArgs* a) {
+    if (!(sc->softcap >= 0.0f) || sc->softcap > 1.0e30f) return fail_in(fn, BG_ERR_SHAPE, "softcap must be at least 0 and at most 1e30");
+    if (tree && (sc->slopes || sc->prefix_lens)) return fail_in(fn, BG_ERR_UNSUPPORTED, "slopes or prefix_lens with a tree");
+    if (!aligned(sc->slopes, 4) || !aligned(sc->prefix_lens, 4)) return fail_in(fn, BG_ERR_ALIGN, "slopes and prefix_lens must be 4-byte aligned");
+    a->cap = sc->softcap * 0x1.715476p0f;
+    a->cap_inv = a->cap > 0.0f ? 1.0f / a->cap : 0.0f;
+    a->slopes = sc->slopes;
+    a->prefix = sc->prefix_lens;
+    a->scored = a->cap > 0.0f || a->slopes || a->prefix;
+    return BG_OK;
+}
+
+bg_status kv_attn_impl(const char* fn, const bg_kv_attn* p, bool tree, const bg_kv_scores* sc, void* ws, int64_t ws_bytes, void* stream) {
     bg::KvAttnArgs a{};
-    const bg_status st = kv_attn_args(fn, p, tree, true, &a);
+    bg_status st = kv_attn_args(fn, p, tree, true, &a);
+    if (st == BG_OK && sc) st = kv_scores(fn, sc, tree, &a);
     if (st != BG_OK) return st;
     if (a.tokens == 0 || a.batch == 0) {
         g_last_error[0] = '\0';
@@ -746,11 +761,17 @@ BG_EXPORT bg_status kv_cache_read(const bg_kv_cache* cache, const int64_t* slots
 }
 
 BG_EXPORT bg_status kv_attn(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream) {
-    return kv_attn_impl("kv_attn", args, false, workspace, workspace_bytes, stream);
+    return kv_attn_impl("kv_attn", args, false, nullptr, workspace, workspace_bytes, stream);
 }
 
 BG_EXPORT bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream) {
-    return kv_attn_impl("kv_attn_tree", args, true, workspace, workspace_bytes, stream);
+    return kv_attn_impl("kv_attn_tree", args, true, nullptr, workspace, workspace_bytes, stream);
+}
+
+BG_EXPORT bg_status kv_attn_scored(const bg_kv_attn* args, const bg_kv_scores* scores, void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "kv_attn_scored";
+    if (!scores) return fail_in(fn, BG_ERR_NULL, "scores must be non-NULL");
+    return kv_attn_impl(fn, args, args && args->tree_words > 0, scores, workspace, workspace_bytes, stream);
 }
 
 BG_EXPORT int64_t kv_attn_workspace_bytes(const bg_kv_attn* args) {
@@ -763,8 +784,6 @@ BG_EXPORT int64_t kv_attn_workspace_bytes(const bg_kv_attn* args) {
 namespace {
 
 constexpr int64_t kMaxPoolPages = int64_t(1) << 30;
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // The pool of `fn`, checked.
 bg_status kv_pool_of(const char* fn, const bg_kv_pool* p, bg::KvPool* out) {

@@ -81,8 +81,8 @@ struct Tile {
 };
 
 // RT row tiles of 16 rows per wave.
-template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+template <int FMT, int D, int RT, bool SCORED>
+__device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     constexpr int DT = D / 16, ST = D / 32, PAD = D + 4;
     // One tile in flight, not two; there a branch spares the products' 8 multiplications by fb for each
@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.c.heads, split = blockIdx.y;
     KvBlock own;
-    if (!kv_block(a, blockIdx.x / a.c.heads, 16 * RT, own)) return;
+    if (!kv_block<SCORED>(a, blockIdx.x / a.c.heads, 16 * RT, own)) return;
     const KvSeq q = own.q;
     const int G = a.q_heads / a.c.heads, rows = own.rows, r0 = own.r0, b = own.b;
     const int last = (rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1;
-    const KvRange rg = kv_range<32>(a, q, r0 / G, last / G);
+    const KvRange rg = kv_range<32, SCORED>(a, q, r0 / G, last / G);
     const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
     const int32_t* table = a.table + b * a.max_pages;
 
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     float rq[RT], m[RT], l[RT], fb[RT];
     bool apart = false;                   // some fb is not 1
     int qi[RT];
+    float slope[SCORED ? RT : 1];         // of the row's head, base 2
     float4_t o[RT][DT];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
         qi[x] = (ok ? row : rows - 1) / G;
         const int64_t at = (q.q0 + qi[x]) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs;
         rq[x] = load_query<FMT, D>(a, at, g, ok, qf[x]);
+        if constexpr (SCORED) slope[x] = a.slopes ? a.slopes[h * G + (ok ? row % G : 0)] * 0x1.715476p0f : 0.0f;
         m[x] = kNoRef;
         l[x] = 0.0f;
         fb[x] = 1.0f;
@@ -186,11 +188,24 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
                 kr[j] = kv_scale<FMT>(t.ks[j]) * rq[x];
                 sv[j] = kv_scale<FMT>(t.vs[j]);
             }
+            if constexpr (SCORED) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = rounded_product(y[j], kr[j]);
+                    kr[j] = 1.0f;
+                }
+                if (a.cap != 0.0f) cap_scores(y, a.cap, a.cap_inv);
+                if (a.slopes) {
+                    const float away = (float)(q.first + qi[x] - first_token);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(-__builtin_fabsf(away - (float)((j & 3) + 16 * (j >> 2))), slope[x], y[j]);
+                }
+            }
             if (!whole) {
                 uint32_t see = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    see |= (uint32_t)((t.there >> (j >> 2) & 1) && kv_sees(a, q, qi[x], first_token + (j & 3) + 16 * (j >> 2))) << j;
+                    see |= (uint32_t)((t.there >> (j >> 2) & 1) && kv_sees<SCORED>(a, q, qi[x], first_token + (j & 3) + 16 * (j >> 2))) << j;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const bool in = see >> j & 1;
@@ -362,6 +377,16 @@ __global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, Kv
     }
 }
 
+template <int FMT, int D, int RT>
+__global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    attend_few<FMT, D, RT, false>(a, sp, po, pl);
+}
+
+template <int FMT, int D, int RT>
+__global__ void __launch_bounds__(kWaves * 64, 2) k_kv_attn_few_scored(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    attend_few<FMT, D, RT, true>(a, sp, po, pl);
+}
+
 // Joins the splits of a row: o = sum_s 2^(ls_s - max) o_s / sum_s 2^(ls_s - max).
 // WPR waves take a row's splits in turn (64 splits one after the other: 18 us), eight
 // partials in flight each.  A split without tokens wrote no partial: its weight is 0
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(256) k_kv_attn_join(KvAttnArgs a, int splits, 
     __shared__ float part[WPR == 1 ? 1 : 4][D];
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.y;
-    const KvSeq q = kv_seq(a, b);
+    const KvSeq q = kv_seq<false>(a, b);
     const int64_t n = a.tokens * a.q_heads, rows = (int64_t)kv_rows(a, q) * a.c.heads, first_row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
     int64_t row = first_row;
     if (row >= rows) return;
@@ -523,8 +548,12 @@ const char* launch_kv_attn(const KvAttnArgs& given, void* ws, hipStream_t s) {
     const char* name = nullptr;
     if (p.waves) name = launch_kv_attn_many(a, p.sp, p.row_blocks, p.waves, po, pl, s);
     else for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
-        if (p.rt == 1) k_kv_attn_few<FMT(), D(), 1><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
-        else if constexpr (D() != 256) k_kv_attn_few<FMT(), D(), 2><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
+        auto few = [&](auto RT) {
+            if (a.scored) k_kv_attn_few_scored<FMT(), D(), RT()><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
+            else k_kv_attn_few<FMT(), D(), RT()><<<grid, kWaves * 64, 0, s>>>(a, p.sp, po, pl);
+        };
+        if (p.rt == 1) few(std::integral_constant<int, 1>{});
+        else if constexpr (D() != 256) few(std::integral_constant<int, 2>{});
     });
     if (p.sp.splits > 1) {
         const bool wide = p.sp.splits > 8;
@@ -542,7 +571,7 @@ const char* launch_kv_attn(const KvAttnArgs& given, void* ws, hipStream_t s) {
         else if (a.c.dim == 128) go(std::integral_constant<int, 128>{});
         else go(std::integral_constant<int, 256>{});
     }
-    return name ? name : kname("k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
+    return name ? name : kname(a.scored ? "k_kv_attn_few_scored" : "k_kv_attn_few", a.c.fmt, a.c.dim, p.rt);
 }
 
 }  // namespace bg

@@ -95,6 +95,7 @@ struct ManyPages {
 // Bit j: the row sees position base + j.
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
+template <bool SCORED>
 __device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& q, int i, int base, uint64_t there) {
     uint64_t m;
     if (a.tree) {
@@ -109,13 +110,14 @@ __device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& 
     } else {
         const int at = q.first + i;
         m = low_bits(at + 1 - base);
+        if constexpr (SCORED) m |= low_bits(q.prefix - base);
         if (a.window) m &= ~low_bits(at - base - (int)a.window + 1) | low_bits((int)a.sinks - base);
     }
     return m & there;
 }
 
-template <int FMT, int D, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+template <int FMT, int D, int WAVES, bool SCORED>
+__device__ __forceinline__ void attend_many(const KvAttnArgs& a, const KvSplit& sp, float* po, float* pl) {
     using L = KvLayout<FMT, D>;
     using M = ManyLayout<FMT, D>;
     constexpr int DT = D / 32, ST = D / 16, PARTS = 8 / WAVES;
@@ -125,11 +127,11 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.c.heads, split = blockIdx.y;
     KvBlock own_rows;
-    if (!kv_block(a, gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads, WAVES * kRows, own_rows)) return;     // the longest first
+    if (!kv_block<SCORED>(a, gridDim.x / a.c.heads - 1 - blockIdx.x / a.c.heads, WAVES * kRows, own_rows)) return;     // the longest first
     const KvSeq q = own_rows.q;
     const int G = a.q_heads / a.c.heads, rows = own_rows.rows, r0 = own_rows.r0, b = own_rows.b;
     const int last = (rows < r0 + WAVES * kRows ? rows : r0 + WAVES * kRows) - 1;
-    const KvRange rg = kv_range<kT>(a, q, r0 / G, last / G);
+    const KvRange rg = kv_range<kT, SCORED>(a, q, r0 / G, last / G);
     const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
     const int nt = t1 - t0;               // tiles of this block: number i is tile t0 + i of the range
     if (nt <= 0 && split > 0) {          // nothing left for this split
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     const int w0 = r0 + wave * kRows;     // the wave's first row
     const bool has_rows = w0 < rows;
     const int wlast = rows < w0 + kRows ? rows - 1 : w0 + kRows - 1;
-    const KvRange wr = kv_range<kT>(a, q, (has_rows ? w0 : rows - 1) / G, wlast / G);
+    const KvRange wr = kv_range<kT, SCORED>(a, q, (has_rows ? w0 : rows - 1) / G, wlast / G);
     const int row = w0 + r;
     const bool ok = row < rows;
     const int qi = (ok ? row : rows - 1) / G;
@@ -155,6 +157,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     // own: what its scores lack (scale_queries); apart: some row of the wave has an fb or own other than 1
     float m = kNoRef, fb = 1.0f, l = 0.0f, own = 1.0f;
     bool apart = false;
+    float slope = 0.0f;                    // of the row's head, base 2
+    if constexpr (SCORED) slope = a.slopes ? a.slopes[h * G + (ok ? row - qi * G : 0)] * 0x1.715476p0f : 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = float16_t{} ;
 
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
             o[j % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(j < FV ? fv[j % FV] : value(n, j), p[1][j / DT], o[j % DT], 0, 0, 0);
         p[1][0] = p[1][1] = half8_t{};
     };
-    auto attend = [&](int i, auto U, bool whole, uint64_t seen, float most, auto&& beside) {
+    auto attend = [&](int i, auto U, bool whole, uint64_t seen, float most, int base, auto&& beside) {
         constexpr int u = U();
         const int n = 2 * i + u;
         float sum = 0.0f;
@@ -214,9 +218,22 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
 #pragma unroll
             for (int c = x * ST / 4; c < (x + 1) * ST / 4; ++c) products(c);
             beside(x);
+            if constexpr (SCORED) {
+                float t[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] = rounded_product(s[u][4 * x + j], kn[j] * own);
+                if (a.cap != 0.0f) cap_scores(t, a.cap, a.cap_inv);
+                if (a.slopes) {
+                    const float away = (float)(q.first + qi - base - 32 * u - 4 * g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) t[j] = __builtin_fmaf(-__builtin_fabsf(away - (float)(8 * x + j)), slope, t[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[u][4 * x + j] = t[j];
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][4 * x + j], kn[j], -m));
+                const float w = __builtin_amdgcn_exp2f(SCORED ? s[u][4 * x + j] - m : __builtin_fmaf(s[u][4 * x + j], kn[j], -m));
                 sum += w;
                 p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(w * vn[j]);
             }
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 const float4_t kn = k_scale(n, x), lv = *reinterpret_cast<const float4_t*>(&lds.lv[n >> 1 & 3][32 * (n & 1) + 8 * x + 4 * g]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float y = rounded_product(s[u][4 * x + j], kn[j] * own);
+                    const float y = SCORED ? s[u][4 * x + j] : rounded_product(s[u][4 * x + j], kn[j] * own);
                     ty = in(x, j) ? __builtin_fmaxf(ty, y) : ty;
                     tp = in(x, j) ? __builtin_fmaxf(tp, y + lv[j]) : tp;
                 }
@@ -266,7 +283,8 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
                 for (int j = 0; j < 4; ++j) {
                     // what the row does not see weighs 0, whatever its scales hold; scores are rounded, as the
                     // reference is: past 2^31 a product's last half step would be a weight of infinity
-                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(rounded_product(s[u][4 * x + j], kn[j] * own) - m) : 0.0f;
+                    const float y = SCORED ? s[u][4 * x + j] : rounded_product(s[u][4 * x + j], kn[j] * own);
+                    const float w = in(x, j) ? __builtin_amdgcn_exp2f(y - m) : 0.0f;
                     sum += w;
                     p[u][x >> 1][4 * (x & 1) + j] = (_Float16)(in(x, j) ? w * (vn[j] * fb) : 0.0f);
                 }
@@ -440,10 +458,10 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
         const bool whole = (th0 == ~0ull) & wr.whole(base, kT);
         uint64_t seen = ~0ull;
         const float next = lds.most[(i + 1) & 3];
-        if (!whole) seen = seen_bits(a, q, qi, base, th0);
+        if (!whole) seen = seen_bits<SCORED>(a, q, qi, base, th0);
         if (has_rows) {
-            attend(i, std::integral_constant<int, 0>{}, whole, seen, most, carry_keys);
-            attend(i, std::integral_constant<int, 1>{}, whole, seen, most, carry_values);
+            attend(i, std::integral_constant<int, 0>{}, whole, seen, most, base, carry_keys);
+            attend(i, std::integral_constant<int, 1>{}, whole, seen, most, base, carry_values);
         } else {
 #pragma unroll
             for (int x = 0; x < 4; ++x) carry_keys(x);
@@ -494,19 +512,33 @@ __global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(K
     }
 }
 
+template <int FMT, int D, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    attend_many<FMT, D, WAVES, false>(a, sp, po, pl);
+}
+
+template <int FMT, int D, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, D == 256 ? 1 : 2) k_kv_attn_many_scored(KvAttnArgs a, KvSplit sp, float* po, float* pl) {
+    attend_many<FMT, D, WAVES, true>(a, sp, po, pl);
+}
+
 }  // namespace
 
 const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s) {
     const dim3 grid((unsigned)a.c.heads * row_blocks, (unsigned)sp.splits, kv_grid_z(a));
     for_format(a.c.fmt, a.c.dim, [&](auto FMT, auto D) {
+        auto many = [&](auto WAVES) {
+            if (a.scored) k_kv_attn_many_scored<FMT(), D(), WAVES()><<<grid, WAVES() * 64, 0, s>>>(a, sp, po, pl);
+            else k_kv_attn_many<FMT(), D(), WAVES()><<<grid, WAVES() * 64, 0, s>>>(a, sp, po, pl);
+        };
         if constexpr (D() != 256) {
-            if (waves == 8) k_kv_attn_many<FMT(), D(), 8><<<grid, 8 * 64, 0, s>>>(a, sp, po, pl);
+            if (waves == 8) many(std::integral_constant<int, 8>{});
         }
         if constexpr (D() != 128) {
-            if (waves == 4) k_kv_attn_many<FMT(), D(), 4><<<grid, 4 * 64, 0, s>>>(a, sp, po, pl);
+            if (waves == 4) many(std::integral_constant<int, 4>{});
         }
     });
-    return kname("k_kv_attn_many", a.c.fmt, a.c.dim, waves);
+    return kname(a.scored ? "k_kv_attn_many_scored" : "k_kv_attn_many", a.c.fmt, a.c.dim, waves);
 }
 
 }  // namespace bg

@@ -32,7 +32,7 @@ EXPORTS = (
     "gemm_w8a8_ex", "gemm_w8a8_ws", "gemm_w8a8_workspace_bytes", "gemm_w4a8", "gemm_w4a8_ws", "gemm_w4a8_workspace_bytes",
     "gemm_w4a16_algo", "gemm_w8a8_algo",
     "kv_cache_write", "kv_cache_read", "kv_attn", "kv_attn_tree", "kv_attn_workspace_bytes",
-    "kv_plan", "kv_release", "qk_norm_rope", "kv_cache_write_rope",
+    "kv_attn_scored", "kv_plan", "kv_release", "qk_norm_rope", "kv_cache_write_rope",
     "bg_status_string", "bg_last_error",
     "bg_pack_format_version", "bg_last_kernel",
 )
@@ -91,6 +91,7 @@ def lib() -> ctypes.CDLL:
             "kv_attn": [P, P, I64, P],
             "kv_attn_tree": [P, P, I64, P],
             "kv_attn_workspace_bytes": [P],
+            "kv_attn_scored": [P, P, P, I64, P],
             "kv_plan": [P, P, I64, I, P, P, P, P, P, P],
             "kv_release": [P, P, P],
             "qk_norm_rope": [P, P],
@@ -484,6 +485,7 @@ def gemm_w8a8_algo(M: int, N: int, K: int, fp8: bool = False) -> int:
 
 _KV_CACHE = struct.Struct("@PPPPqiiii")               # bg_kv_cache
 _KV_ATTN = struct.Struct("@PPqqPqPPPPPqqqqqqiiif")    # bg_kv_attn
+_KV_SCORES = struct.Struct("@PPf4x")                  # bg_kv_scores
 _KV_DIMS = (64, 128, 256)
 
 
@@ -650,7 +652,8 @@ def _kv_workspace(nbytes: int, device, stream: int) -> torch.Tensor:
     return ws
 
 
-def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, window, sinks, scale, out, lse, ws):
+def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, window, sinks, scale, out, lse, ws, softcap=0.0, slopes=None,
+             prefix_lens=None):
     if q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.head_dim:
         raise ValueError(f"{fn}: q must be [T][q_heads][{cache.head_dim}] with a contiguous last axis, got {tuple(q.shape)}")
     T, heads, dim = q.shape
@@ -678,9 +681,14 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
         raise ValueError(f"{fn}: out must be a contiguous {(T, heads, dim)} of {q.dtype}")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, heads) or not lse.is_contiguous()):
         raise ValueError(f"{fn}: lse must be a contiguous float32 {(T, heads)}")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (heads,) or not slopes.is_contiguous()):
+        raise ValueError(f"{fn}: slopes must be a contiguous float32 vector of {heads}")
+    if prefix_lens is not None:
+        _int32(fn, prefix_lens, (B,), "prefix_lens")
+    scored = softcap != 0.0 or slopes is not None or prefix_lens is not None
     if T == 0 or B == 0:
         return out
-    _on_device(fn, cache, q, block_table, kv_lens, cu_q, tree, out, lse, ws)
+    _on_device(fn, cache, q, block_table, kv_lens, cu_q, tree, out, lse, ws, slopes, prefix_lens)
     L = lib()
     s = _raw_stream(cache.device.index)
     args = _KV_ATTN.pack(
@@ -694,14 +702,20 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
         ws = _kv_workspace(need, q.device, s) if need > 0 else None
     elif not ws.is_contiguous():
         raise ValueError(f"{fn}: the workspace must be contiguous")
-    _check(getattr(L, fn)(args, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), s), fn)
+    room = None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size()
+    if scored:
+        scores = _KV_SCORES.pack(0 if slopes is None else slopes.data_ptr(), 0 if prefix_lens is None else prefix_lens.data_ptr(), softcap)
+        _check(L.kv_attn_scored(args, scores, *room, s), fn)
+    else:
+        _check(getattr(L, fn)(args, *room, s), fn)
     return out
 
 
 def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
             cu_q: torch.Tensor | None = None, max_q_len: int | None = None, *, max_kv_len: int = 0, window: int = 0, sinks: int = 0,
             scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-            ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+            ws: torch.Tensor | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+            prefix_lens: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention of ragged queries [T][q_heads][D] over the cache -> [T][q_heads][D].
 
     Sequence b owns the queries cu_q[b] .. cu_q[b + 1] - 1 (cu_q None: one query
@@ -715,19 +729,23 @@ def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens:
     cu_q costs some speed.  scale None: D ** -0.5.  lse: float32
     [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
     workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream
-    (a captured graph: its own)."""
+    (a captured graph: its own).
+
+    softcap > 0 caps a scaled score t to softcap * tanh(t / softcap); slopes
+    float32 [q_heads] then takes slopes[h] * |own position - j| off it; with prefix_lens int32
+    [batch] a query sees the positions below prefix_lens[b] behind its own, too."""
     if stream is not None:
-        return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, out, lse, ws),
+        return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, out, lse, ws, slopes, prefix_lens),
                           lambda: kv_attn(q, cache, block_table, kv_lens, cu_q, max_q_len, max_kv_len=max_kv_len, window=window,
-                                          sinks=sinks, scale=scale, out=out, lse=lse, ws=ws))
+                                          sinks=sinks, scale=scale, out=out, lse=lse, ws=ws, softcap=softcap, slopes=slopes, prefix_lens=prefix_lens))
     return _kv_attn("kv_attn", q, cache, block_table, kv_lens, cu_q, None, max_q_len, max_kv_len, window, sinks, scale, out,
-                    lse, ws)
+                    lse, ws, softcap, slopes, prefix_lens)
 
 
 def kv_attn_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor,
                  tree: torch.Tensor, max_q_len: int, *, max_kv_len: int = 0, scale: float | None = None,
                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 softcap: float = 0.0, stream=None) -> torch.Tensor:
     """kv_attn for a tree of drafted tokens: a sequence's queries are its last
     positions (already written), each sees every position before them, and of
     the drafted ones exactly its bits of tree int64 [T][words] (bit e % 64 of word
@@ -736,8 +754,8 @@ def kv_attn_tree(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_
         return _on_stream(stream, (q, cache.k, cache.v, cache.k_scales, cache.v_scales, block_table, kv_lens, cu_q, tree, out,
                                    lse, ws),
                           lambda: kv_attn_tree(q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len=max_kv_len,
-                                               scale=scale, out=out, lse=lse, ws=ws))
-    return _kv_attn("kv_attn_tree", q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, 0, 0, scale, out, lse, ws)
+                                               scale=scale, out=out, lse=lse, ws=ws, softcap=softcap))
+    return _kv_attn("kv_attn_tree", q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_len, 0, 0, scale, out, lse, ws, softcap)
 
 
 def kv_attn_workspace_bytes(q_shape, cache: KVCache, batch: int, max_pages: int, max_q_len: int | None = None, max_kv_len: int = 0,

@@ -597,6 +597,27 @@ typedef struct bg_kv_attn {
 bg_status kv_attn(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream);
 bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * kv_attn_scored -- kv_attn (args->tree_words == 0) or kv_attn_tree (> 0) with
+ * other scores.  Of the score t = scale * (q, k) of a query at position own and
+ * position j becomes
+ *   t <- softcap * tanh(t / softcap)        softcap > 0 (at most 1e30); 0: not
+ *   t <- t - slopes[h] * |own - j|          slopes [q_heads] binary32, finite; NULL: not
+ * and with prefix_lens [batch] a query of sequence b sees the positions below
+ * prefix_lens[b] (clamped to 0 .. kv_lens[b]) that lie behind its own, too: j <= own or j <
+ * prefix_lens[b], and the window as before.  With a tree softcap only.
+ * Computed in binary32 (tanh within 2^-21 of its value; distances beyond 2^24 within 2^-23 of theirs).
+ * Same workspace as kv_attn / kv_attn_tree.
+ */
+typedef struct bg_kv_scores {
+    const float* slopes;
+    const int32_t* prefix_lens;
+    float softcap;
+} bg_kv_scores;
+
+bg_status kv_attn_scored(const bg_kv_attn* args, const bg_kv_scores* scores, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
 /* Workspace bytes of kv_attn (tree_words == 0) or kv_attn_tree (tree_words > 0)
  * for these arguments: 0 if none, or if the arguments are not eligible.  Reads
  * sizes only: apart from cache and cu_q (NULL or not), pointers may be NULL. */

@@ -192,3 +192,30 @@ def test_reference_turn():
     y = ref.turn(np.full((1, 1, 4), 3.0), np.full(4, 0.5), [0], [], eps=7.0, offset=1.0)
     assert np.allclose(y, 3 / math.sqrt(16) * 1.5)
     assert F32 == 0
+
+
+# ---- attention with other scores ----
+
+class Scores(ctypes.Structure):
+    _fields_ = [("slopes", VP), ("prefix_lens", VP), ("softcap", ctypes.c_float)]
+
+
+def test_scores_are_checked(L):
+    from test_kv_cpu import E_UNSUP, E_WS, attn
+    from bit_gemm_w4_amd import ops
+    assert ops._KV_SCORES.size == ctypes.sizeof(Scores)
+    c = cache()
+    call = lambda a, s: L.kv_attn_scored(ctypes.addressof(a), ctypes.addressof(s), P, 1 << 40, None)  # noqa: E731
+    a, tree = attn(c), attn(c, tree_words=1, tree=P)
+    for s, status in ((Scores(None, None, -1.0), E_SHAPE), (Scores(None, None, float("nan")), E_SHAPE), (Scores(None, None, 2e30), E_SHAPE),
+                      (Scores(P + 2, None, 1.0), E_ALIGN), (Scores(None, P + 1, 1.0), E_ALIGN)):
+        assert call(a, s) == status
+        assert L.bg_last_error().decode().startswith("kv_attn_scored: ")
+    assert call(tree, Scores(P, None, 0.0)) == E_UNSUP and call(tree, Scores(None, P, 1.0)) == E_UNSUP
+    assert L.kv_attn_scored(ctypes.addressof(a), None, P, 1 << 40, None) == E_NULL
+    assert L.kv_attn_scored(None, ctypes.addressof(Scores()), P, 1 << 40, None) == E_NULL
+    assert call(attn(c, max_q=0), Scores(None, None, 1.0)) == E_SHAPE
+    assert call(attn(c, tokens=0), Scores(P, P, 1.0)) == OK
+    big = cache(pages=100000, kv_heads=8)
+    long = attn(big, tokens=1, batch=1, max_q=1, cu_q=None, q_heads=32, max_pages=8192)
+    assert L.kv_attn_scored(ctypes.addressof(long), ctypes.addressof(Scores(P, None, 0.0)), None, 0, None) == E_WS
