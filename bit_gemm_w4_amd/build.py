@@ -38,7 +38,7 @@ FLAGS = [
 FILE_FLAGS = {
     "k_w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "k_kvattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-    "k_kvattn_many.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    **{f"k_kvattn_many{x}.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"] for x in ("", "_bias", "_cap", "_cap_bias", "_far_cap")},
     "k_w8a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

@@ -79,7 +79,8 @@ struct KvAttnArgs {
     void* out;                 // [tokens][q_heads][D]
     float* lse;                // [tokens][q_heads], or NULL
     bool scored;               // any of the following
-    float cap, cap_inv;        // scores are capped: cap tanh(score cap_inv), in base-2 units; 0: not
+    float cap, cap_inv;        // scores (base 2) are capped: cap tanh(score cap_inv); cap_inv 0: not, cap 1
+    bool cap_far;              // a cap of kCapExp (bg_kvattn.h) or more
     const float* slopes;       // [q_heads]: less slope times distance; or NULL
     const int32_t* prefix;     // [batch]: positions below it are seen from before, too; or NULL
 };

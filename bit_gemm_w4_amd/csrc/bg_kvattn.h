@@ -244,34 +244,61 @@ __device__ __forceinline__ RowStep raise_row(float& m, float& fb, float ty, floa
     return f;
 }
 
-// Scores t (base 2) to cap tanh(t / cap).  Where no lane's |u| = |t| / cap passes 1, as usually
-// with the caps in use, tanh(u) / u is a polynomial in u^2 (a minimax fit, off by 2^-24):
-// 9 vector instructions a score; beyond, 1 - 2 / (1 + e^2|u|) beside it, whose two
-// transcendentals cost as much as 8 others.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&t)[N], float cap, float inv) {
-    float u[N], top = 0.0f;
+// The slope of a head's bias, in units of the scores before their last factor, a.cap.  With slopes the
+// tiles are taken from the last one back: a query's nearest positions usually hold its largest scores, so its
+// references seldom move after the first (forwards, in every tile of a steep head: 2,048 queries over a window
+// of 4,096, E4M3, 32 heads of 128, slopes 2^(-i / 4): 395 us, 188 so).
+__device__ __forceinline__ float head_slope(const KvAttnArgs& a, int head) { return a.slopes[head] * 0x1.715476p0f * (a.cap_inv != 0.0f ? a.cap_inv : 1.0f); }
+
+// Caps up to kCapExp are taken as tanh(u) = 1 - 2 / (1 + 2^x), x = 2 log2(e) u (a factor that the tokens'
+// scales take along): within 2^-21, so a score errs by 2^-21 of its cap, a weight by 2^-13 of itself at most, of
+// which FP16 takes 2^-11.  Larger ones (FAR) as polynomials, within 2^-21 of tanh(u).  Those have fewer vector
+// instructions, 6 a score against what 10 take, but they need their largest score looked at: with a branch
+// on it in the loop the above chunk with a cap of 50 took 288 us, by the power it takes 218.
+constexpr float kCapExp = 256.0f;
+__device__ __forceinline__ float cap_unit(const KvAttnArgs& a) { return a.cap_far ? a.cap_inv : a.cap_inv * 0x1.715476p1f; }
+
+// tanh(u) / u for z = u^2 (minimax polynomials): |u| up to kTanhSmall, off by 2^-22.2, and up to 1, by 2^-22.6.
+constexpr float kTanhSmall = 0.4f;
+
+__device__ __forceinline__ float tanh_ratio_small(float z) {
+    float p = -0x1.858f22p-5f;
+    p = __builtin_fmaf(p, z, 0x1.0fca24p-3f);
+    p = __builtin_fmaf(p, z, -0x1.55502ap-2f);
+    return __builtin_fmaf(p, z, 0x1.fffffcp-1f);
+}
+
+__device__ __forceinline__ float tanh_ratio(float z) {
+    float p = 0x1.10e5d6p-10f;
+    p = __builtin_fmaf(p, z, -0x1.968b6cp-8f);
+    p = __builtin_fmaf(p, z, 0x1.4c6e58p-6f);
+    p = __builtin_fmaf(p, z, -0x1.b5eb84p-5f);
+    p = __builtin_fmaf(p, z, 0x1.10e672p-3f);
+    p = __builtin_fmaf(p, z, -0x1.55540ap-2f);
+    return __builtin_fmaf(p, z, 0x1.fffffep-1f);
+}
+
+// u to tanh(u).  FAR: where scores under large caps lie, by a polynomial; if some score of the wave is larger, by
+// another up to 1 and as below beyond, for all.
+template <bool FAR, int N>
+__device__ __forceinline__ void cap_scores(float (&u)[N]) {
+    float top = 0.0f;
+    if constexpr (FAR) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        u[j] = t[j] * inv;
-        top = __builtin_fmaxf(top, __builtin_fabsf(u[j]));
-        const float z = u[j] * u[j];
-        float p = 0x1.10e5d6p-10f;
-        p = __builtin_fmaf(p, z, -0x1.968b6cp-8f);
-        p = __builtin_fmaf(p, z, 0x1.4c6e58p-6f);
-        p = __builtin_fmaf(p, z, -0x1.b5eb84p-5f);
-        p = __builtin_fmaf(p, z, 0x1.10e672p-3f);
-        p = __builtin_fmaf(p, z, -0x1.55540ap-2f);
-        p = __builtin_fmaf(p, z, 0x1.fffffep-1f);
-        t[j] *= p;
+        for (int j = 0; j < N; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(u[j]));
     }
-    if (__any(top > 1.0f)) {
+    if constexpr (!FAR) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) u[j] = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u[j])), 1.0f);
+    } else if (__any(top > kTanhSmall)) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(u[j]) * 0x1.715476p1f);
-            const float y = cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
-            t[j] = __builtin_fabsf(u[j]) > 1.0f ? __builtin_copysignf(y, u[j]) : t[j];
+            const float x = u[j], y = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(__builtin_fabsf(x) * 0x1.715476p1f));
+            u[j] = __builtin_fabsf(x) > 1.0f ? __builtin_copysignf(y, x) : x * tanh_ratio(x * x);
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) u[j] *= tanh_ratio_small(u[j] * u[j]);
     }
 }
 
@@ -520,5 +547,10 @@ inline unsigned kv_grid_z(const KvAttnArgs& a) { return (unsigned)(a.batch + (a.
 
 // Many query rows per kv head, rows of row_blocks blocks of 8 waves (4 at D = 256; either at D = 64) (k_kvattn_many.hip).
 const char* launch_kv_attn_many(const KvAttnArgs& a, const KvSplit& sp, unsigned row_blocks, int waves, float* po, float* pl, hipStream_t s);
+// With other scores (k_kvattn_many_*.hip): biased (or none but a prefix), capped, both, far caps with or without a bias.
+void launch_kv_attn_many_bias(const KvAttnArgs& a, const KvSplit& sp, dim3 grid, int waves, float* po, float* pl, hipStream_t s);
+void launch_kv_attn_many_cap(const KvAttnArgs& a, const KvSplit& sp, dim3 grid, int waves, float* po, float* pl, hipStream_t s);
+void launch_kv_attn_many_cap_bias(const KvAttnArgs& a, const KvSplit& sp, dim3 grid, int waves, float* po, float* pl, hipStream_t s);
+void launch_kv_attn_many_far_cap(const KvAttnArgs& a, const KvSplit& sp, dim3 grid, int waves, float* po, float* pl, hipStream_t s);
 
 }  // namespace bg

@@ -685,14 +685,16 @@ bg_status kv_attn_args(const char* fn, const bg_kv_attn* p, bool tree, bool poin
 
 // What `sc` asks of the scores, checked.
 bg_status kv_scores(const char* fn, const bg_kv_scores* sc, bool tree, bg::KvAttnArgs* a) {
-    if (!(sc->softcap >= 0.0f) || sc->softcap > 1.0e30f) return fail_in(fn, BG_ERR_SHAPE, "softcap must be at least 0 and at most 1e30");
+    if (!(sc->softcap >= 0.0f) || sc->softcap > 1.0e30f || (sc->softcap > 0.0f && sc->softcap < 1.0e-30f))
+        return fail_in(fn, BG_ERR_SHAPE, "softcap must be 0 or lie in 1e-30 .. 1e30");
     if (tree && (sc->slopes || sc->prefix_lens)) return fail_in(fn, BG_ERR_UNSUPPORTED, "slopes or prefix_lens with a tree");
     if (!aligned(sc->slopes, 4) || !aligned(sc->prefix_lens, 4)) return fail_in(fn, BG_ERR_ALIGN, "slopes and prefix_lens must be 4-byte aligned");
-    a->cap = sc->softcap * 0x1.715476p0f;
-    a->cap_inv = a->cap > 0.0f ? 1.0f / a->cap : 0.0f;
+    const bool caps = sc->softcap > 0.0f;
+    a->cap = caps ? (float)(sc->softcap * 0x1.71547652b82fep0) : 1.0f;
+    a->cap_inv = caps ? (float)(1.0 / (sc->softcap * 0x1.71547652b82fep0)) : 0.0f;
     a->slopes = sc->slopes;
     a->prefix = sc->prefix_lens;
-    a->scored = a->cap > 0.0f || a->slopes || a->prefix;
+    a->scored = caps || a->slopes || a->prefix;
     return BG_OK;
 }
 

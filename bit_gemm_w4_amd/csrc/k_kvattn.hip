@@ -112,9 +112,10 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
         return;
     }
 
+    auto tile_of = [&](int i) { return rg.tile(SCORED && a.slopes ? t0 + t1 - 1 - i : i); };      // see head_slope
     // a tile's pages are looked up two tiles before its codes are asked for
     auto find = [&](int (&page)[2], int i) {
-        const int base = rg.tile(i < t1 ? i : t1 - 1) * 32;
+        const int base = tile_of(i < t1 ? i : t1 - 1) * 32;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int64_t p = (base + 16 * s) >> a.c.page_shift;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
     float rq[RT], m[RT], l[RT], fb[RT];
     bool apart = false;                   // some fb is not 1
     int qi[RT];
-    float slope[SCORED ? RT : 1];         // of the row's head, base 2
+    float slope[SCORED ? RT : 1];         // of the row's head (head_slope)
     float4_t o[RT][DT];
 #pragma unroll
     for (int x = 0; x < RT; ++x) {
@@ -142,7 +143,10 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
         qi[x] = (ok ? row : rows - 1) / G;
         const int64_t at = (q.q0 + qi[x]) * a.q_ts + (h * G + (ok ? row % G : 0)) * a.q_hs;
         rq[x] = load_query<FMT, D>(a, at, g, ok, qf[x]);
-        if constexpr (SCORED) slope[x] = a.slopes ? a.slopes[h * G + (ok ? row % G : 0)] * 0x1.715476p0f : 0.0f;
+        if constexpr (SCORED) {
+            rq[x] = a.cap_inv != 0.0f ? rq[x] * cap_unit(a) : rq[x];
+            slope[x] = a.slopes ? head_slope(a, h * G + (ok ? row % G : 0)) : 0.0f;
+        }
         m[x] = kNoRef;
         l[x] = 0.0f;
         fb[x] = 1.0f;
@@ -189,12 +193,16 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
                 sv[j] = kv_scale<FMT>(t.vs[j]);
             }
             if constexpr (SCORED) {
+                // score j is y[j] cap from here on
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     y[j] = rounded_product(y[j], kr[j]);
-                    kr[j] = 1.0f;
+                    kr[j] = a.cap;
                 }
-                if (a.cap != 0.0f) cap_scores(y, a.cap, a.cap_inv);
+                if (a.cap_inv != 0.0f) {
+                    if (a.cap_far) cap_scores<true>(y);
+                    else cap_scores<false>(y);
+                }
                 if (a.slopes) {
                     const float away = (float)(q.first + qi[x] - first_token);
 #pragma unroll
@@ -293,26 +301,26 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
         // 113, 172 and 79; 18 x 2 queries of 4668, 4 bits, D = 256, 55, 44 and 45.
         Tile<FMT, D> t;
         for (; i < t1; i += kWaves) {
-            t.load(a, pa, h, rg.tile(i), r, g);
+            t.load(a, pa, h, tile_of(i), r, g);
             pa[0] = pb[0];
             pa[1] = pb[1];
             find(pb, i + 2 * kWaves);
-            compute(t, rg.tile(i));
+            compute(t, tile_of(i));
         }
     } else {
         Tile<FMT, D> ta, tb;
         if (i < t1) {
-            ta.load(a, pa, h, rg.tile(i), r, g);
+            ta.load(a, pa, h, tile_of(i), r, g);
             find(pa, i + 2 * kWaves);
         }
         for (; i < t1; i += 2 * kWaves) {
-            if (i + kWaves < t1) tb.load(a, pb, h, rg.tile(i + kWaves), r, g);
+            if (i + kWaves < t1) tb.load(a, pb, h, tile_of(i + kWaves), r, g);
             find(pb, i + 3 * kWaves);
-            compute(ta, rg.tile(i));
+            compute(ta, tile_of(i));
             if (i + kWaves >= t1) break;
-            if (i + 2 * kWaves < t1) ta.load(a, pa, h, rg.tile(i + 2 * kWaves), r, g);
+            if (i + 2 * kWaves < t1) ta.load(a, pa, h, tile_of(i + 2 * kWaves), r, g);
             find(pa, i + 4 * kWaves);
-            compute(tb, rg.tile(i + kWaves));
+            compute(tb, tile_of(i + kWaves));
         }
     }
 
@@ -542,6 +550,7 @@ const char* launch_kv_attn(const KvAttnArgs& given, void* ws, hipStream_t s) {
     const Plan p = plan_of(given);
     KvAttnArgs a = given;
     a.chunk = p.chunk;
+    a.cap_far = a.cap_inv != 0.0f && a.cap > kCapExp * 0x1.715476p0f;
     float* po = static_cast<float*>(ws);
     float* pl = po + (int64_t)p.sp.splits * a.tokens * a.q_heads * a.c.dim;
     const dim3 grid((unsigned)a.c.heads * p.row_blocks, (unsigned)p.sp.splits, kv_grid_z(a));

@@ -601,12 +601,12 @@ bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspac
  * kv_attn_scored -- kv_attn (args->tree_words == 0) or kv_attn_tree (> 0) with
  * other scores.  Of the score t = scale * (q, k) of a query at position own and
  * position j becomes
- *   t <- softcap * tanh(t / softcap)        softcap > 0 (at most 1e30); 0: not
+ *   t <- softcap * tanh(t / softcap)        softcap 1e-30 .. 1e30; 0: not
  *   t <- t - slopes[h] * |own - j|          slopes [q_heads] binary32, finite; NULL: not
  * and with prefix_lens [batch] a query of sequence b sees the positions below
  * prefix_lens[b] (clamped to 0 .. kv_lens[b]) that lie behind its own, too: j <= own or j <
  * prefix_lens[b], and the window as before.  With a tree softcap only.
- * Computed in binary32 (tanh within 2^-21 of its value; distances beyond 2^24 within 2^-23 of theirs).
+ * Computed in binary32 (tanh within 2^-21, for caps beyond 256 2^-21 of its value; distances beyond 2^24 within 2^-23 of theirs).
  * Same workspace as kv_attn / kv_attn_tree.
  */
 typedef struct bg_kv_scores {
