@@ -875,8 +875,7 @@ def kv_plan(pool: KVPool, q_lens: torch.Tensor, tokens: int, *, advance: bool = 
         if tokens < 0:
             raise ValueError(f"{fn}: tokens={tokens} is negative")
         ints = torch.empty(3 * B + 1 + tokens, dtype=torch.int32, device=pool.device)
-        out = KVPlan(ints[:B + 1], ints[B + 1:2 * B + 1], ints[2 * B + 1:3 * B + 1], ints[3 * B + 1:],
-                     torch.empty(tokens, dtype=torch.int64, device=pool.device))
+        out = KVPlan(*ints.split_with_sizes((B + 1, B, B, tokens)), torch.empty(tokens, dtype=torch.int64, device=pool.device))
     else:
         for t, n, name in ((out.cu_q, B + 1, "cu_q"), (out.kv_lens, B, "kv_lens"), (out.served, B, "served"), (out.positions, tokens, "positions")):
             _int32(fn, t, (n,), f"out.{name}")

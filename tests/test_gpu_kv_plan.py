@@ -47,7 +47,8 @@ def same_plan(plan, want):
     (4, 32, 300, 60, 300, 90, 1, 33),             # a window of one token, sinks over a page's end
     (40, 16, 900, 25, 2500, 120, 100, 0),         # several blocks of rows
     (700, 16, 6000, 9, 5000, 9, 30, 17),
-    (4097, 16, 5000, 3, 4096, 2, 0, 0),           # one sequence more than a turn of the sums takes
+    (256, 16, 3000, 9, 300, 5, 40, 3), (257, 16, 3000, 9, 2000, 5, 0, 0), (513, 16, 3000, 9, 1500, 3, 25, 0),      # ends of a turn, of the waves' form
+    (4097, 16, 5000, 3, 4096, 2, 0, 0),           # one sequence more than a turn of the blocks takes
 ])
 def test_random_steps(ops, batch, page, pages, width, tokens, most, window, sinks):
     rng = np.random.default_rng(batch * 1000 + page)
