@@ -91,26 +91,49 @@ __device__ __forceinline__ void store4(void* p, int64_t at, const float* f) {
     }
 }
 
-// Norm and rotation of a lane's eight elements, in T; c and s are those of its pairs.
-template <typename T, int D>
-__device__ __forceinline__ void turn_row(const RopeArgs& a, const float (&x)[8], const float (&w)[8], bool norm, bool turns, const T (&c)[4], const T (&s)[4],
-                                         T (&y)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = (T)x[i];
+// 1 / sqrt(x): the hardware's estimate and a step of Newton's (in binary64 of third order: the
+// estimate is good for 2^-23), 5 operations where the root and the quotient take 20 and more.
+__device__ __forceinline__ float inverse_root(float x) {
+    const float r = __builtin_amdgcn_rsqf(x), e = __builtin_fmaf(-x * r, r, 1.0f);
+    float y = __builtin_fmaf(0.5f * r, e, r);
+    const bool plain = x >= 0x1p-100f && x <= 0x1p100f;
+    if (__any(!plain)) y = plain ? y : 1.0f / __builtin_sqrtf(x);
+    return y;
+}
+
+__device__ __forceinline__ double inverse_root(double x) {
+    const double r = __builtin_amdgcn_rsq(x), e = __builtin_fma(-x * r, r, 1.0);
+    return __builtin_fma(r * e, __builtin_fma(0.375, e, 0.5), r);
+}
+
+// Norm and rotation of a lane's eight elements, in T, a pair at a time; pair n's cosine and sine lie at phase[n * step].
+template <typename T, int D, typename P>
+__device__ __forceinline__ void turn_row(const RopeArgs& a, float (&x)[8], const float (&w)[8], bool norm, bool turns, const P* phase, int step) {
+    T r = 1;
     if (norm) {
         T sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_elementwise_fma(y[i], y[i], sum);
+        for (int i = 0; i < 8; ++i) sum = __builtin_elementwise_fma((T)x[i], (T)x[i], sum);
         sum = over_row<D / 8>(sum, [](T p, T q) { return p + q; });
-        const T r = (T)1 / __builtin_elementwise_sqrt(sum * (T)(1.0 / D) + (T)a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * ((T)w[i] + (T)a.offset);
+        r = inverse_root(sum * (T)(1.0 / D) + (T)a.eps);
     }
-    if (!turns) return;
     auto pair = [&](int i, int j, int n) {
-        const T p = y[i], q = y[j];
-        y[i] = __builtin_elementwise_fma(p, c[n], -(q * s[n]));
-        y[j] = __builtin_elementwise_fma(p, s[n], q * c[n]);
+        float xi = x[i], xj = x[j], wi = w[i], wj = w[j];
+        // binary64 copies that wait in registers would cost waves
+        if constexpr (sizeof(T) == 8) asm volatile("" : "+v"(xi), "+v"(xj), "+v"(wi), "+v"(wj));
+        T p = (T)xi, q = (T)xj;
+        if (norm) {
+            p = p * r * ((T)wi + (T)a.offset);
+            q = q * r * ((T)wj + (T)a.offset);
+        }
+        if (turns) {
+            const P z = phase[n * step];
+            const T c = z.x, s = z.y, u = p;
+            p = __builtin_elementwise_fma(u, c, -(q * s));
+            q = __builtin_elementwise_fma(u, s, q * c);
+        }
+        x[i] = (float)p;
+        x[j] = (float)q;
     };
     if (a.interleaved) {
 #pragma unroll
@@ -142,18 +165,23 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     const int e0 = halves ? 4 * lane : 8 * lane, e1 = halves ? pairs + 4 * lane : 8 * lane + 4;
     const bool turns = kind != ROW_V && lane < a.rot / 8;
 
-    auto token_of = [&](uint32_t i) { return (h0 + i) / (uint32_t)heads; };
-    auto at_of = [&](uint32_t i) {
-        const uint32_t t = token_of(i), h = h0 + i - t * heads;
-        return (int64_t)(t0 + t) * ts + (int64_t)h * hs;
+    // row i's token and head, from the block's first
+    struct At {
+        uint32_t t, h;
+    };
+    auto place = [&](uint32_t i) {
+        const uint32_t t = (h0 + i) / (uint32_t)heads;
+        return At{t, h0 + i - t * heads};
     };
     uint32_t i = threadIdx.x / L;
     Four<DT> x0{}, x1{};
-    if (i < rows) {
-        const int64_t at = at_of(i);
+    At next = place(i);
+    auto ask = [&]() {
+        const int64_t at = (int64_t)(t0 + next.t) * ts + (int64_t)next.h * hs;
         x0 = load4<DT>(src, at + e0);
         x1 = load4<DT>(src, at + e1);
-    }
+    };
+    if (i < rows) ask();
     const void* weight = kind == ROW_Q ? a.q_weight : kind == ROW_K ? a.k_weight : nullptr;
     float w[8];
     if (weight) {
@@ -167,7 +195,7 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     }
     // pair n of token t: phase[t pairs + (n % 4) pairs / 4 + n / 4], so that lanes read next to each other
     if (kind != ROW_V && pairs > 0 && rows > 0) {
-        const uint32_t some = (token_of(rows - 1) + 1) * pairs;
+        const uint32_t some = (place(rows - 1).t + 1) * pairs;
         for (uint32_t n = threadIdx.x; n < some; n += kBlock) {
             const uint32_t t = n / pairs, p = n - t * pairs;
             double c, s;
@@ -182,47 +210,24 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
         float x[8];
         floats4<DT>(x0, x);
         floats4<DT>(x1, x + 4);
-        const uint32_t t = token_of(i), h = h0 + i - t * heads;
+        const uint32_t t = next.t, h = next.h;
         if (i + SLOTS < rows) {
-            const int64_t at = at_of(i + SLOTS);
-            x0 = load4<DT>(src, at + e0);
-            x1 = load4<DT>(src, at + e1);
+            next = place(i + SLOTS);
+            ask();
         }
         const uint32_t from = t * pairs + lane;
         if (!wide && kind != ROW_V) {
-            float c[4] = {}, s[4] = {}, y[8];
-            if (turns) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 z = reinterpret_cast<const float2*>(phase)[from + n * (pairs / 4)];
-                    c[n] = z.x;
-                    s[n] = z.y;
-                }
-            }
-            turn_row<float, D>(a, x, w, weight != nullptr, turns, c, s, y);
+            turn_row<float, D>(a, x, w, weight != nullptr, turns, reinterpret_cast<const float2*>(phase) + from, pairs / 4);
             void* to = kind == ROW_Q ? a.q_out : a.k_out;
             const int64_t at = (int64_t)(t0 + t) * (kind == ROW_Q ? a.qo_ts : a.ko_ts) + (int64_t)h * (kind == ROW_Q ? a.qo_hs : a.ko_hs);
-            store4<DT>(to, at + e0, y);
-            store4<DT>(to, at + e1, y + 4);
+            store4<DT>(to, at + e0, x);
+            store4<DT>(to, at + e1, x + 4);
         }
         if constexpr (FMT != 0) {
             if (kind == ROW_Q) continue;
             const int64_t slot = a.slots[t0 + t];
             if (slot < 0 || slot >= (cache.pages << cache.page_shift)) continue;       // whole rows skip together
-            if (wide) {
-                double c[4] = {}, s[4] = {}, y[8];
-                if (turns) {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const double2 z = phase[from + n * (pairs / 4)];
-                        c[n] = z.x;
-                        s[n] = z.y;
-                    }
-                }
-                turn_row<double, D>(a, x, w, weight != nullptr, turns, c, s, y);
-#pragma unroll
-                for (int n = 0; n < 8; ++n) x[n] = (float)y[n];
-            }
+            if (wide) turn_row<double, D>(a, x, w, weight != nullptr, turns, phase + from, pairs / 4);
             const int64_t row = kv_row(cache, slot, (int)h);
             uint8_t* codes = (kind == ROW_V ? cache.v : cache.k) + row * (FMT == KV_U4 ? D / 2 : D);
             const RowCodes q = quantize_row<FMT, D>(x);

@@ -919,9 +919,24 @@ def rope_freqs(inv_freq) -> torch.Tensor:
 
 def _rope_rows(fn: str, t: torch.Tensor, name: str, tokens: int, dt, dim: int) -> tuple:
     """The token and head strides of rows [tokens][heads][dim]."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or t.dtype != dt or t.stride(2) != 1:
-        raise ValueError(f"{fn}: {name} must be [{tokens}][heads][{dim}] of {dt} with a contiguous last axis, got {t.dtype} {tuple(t.shape)}")
-    return 0 if tokens == 1 else t.stride(0), 0 if t.shape[1] == 1 else t.stride(1)      # an axis of one element may have any stride
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or t.dtype != dt or strides[2] != 1:
+        raise ValueError(f"{fn}: {name} must be [{tokens}][heads][{dim}] of {dt} with a contiguous last axis, got {t.dtype} {tuple(shape)}")
+    if tokens == 1 or shape[1] == 1:       # an axis of one element may have any stride
+        return 0 if tokens == 1 else strides[0], 0 if shape[1] == 1 else strides[1]
+    return strides[:2]
+
+
+def _rope_out(fn: str, t: torch.Tensor | None, out: torch.Tensor | None, name: str) -> torch.Tensor | None:
+    if t is None:
+        if out is not None:
+            raise ValueError(f"{fn}: {name} without its rows")
+        return None
+    if out is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if out.shape != t.shape:
+        raise ValueError(f"{fn}: {name} must be {tuple(t.shape)}, got {tuple(out.shape)}")
+    return out
 
 
 def _qk_rope(fn, q, k, v, cache, slots, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, k_out):
@@ -930,28 +945,17 @@ def _qk_rope(fn, q, k, v, cache, slots, positions, freqs, q_weight, k_weight, ep
         raise ValueError(f"{fn}: queries or keys must be given")
     if x.dim() != 3:
         raise ValueError(f"{fn}: rows must be [tokens][heads][D], got {tuple(x.shape)}")
-    T, dim = x.shape[0], x.shape[2]
-    dt = _TORCH_DT.get(x.dtype)
+    T, _, dim = x.shape
+    dtype = x.dtype
+    dt = _TORCH_DT.get(dtype)
     if dt is None:
-        raise ValueError(f"{fn}: rows must be float32, float16 or bfloat16, got {x.dtype}")
-    strides, ptrs, outs = [], [], []
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        strides += (0, 0) if t is None else _rope_rows(fn, t, name, T, x.dtype, dim)
-        ptrs.append(0 if t is None else t.data_ptr())
-    for t, given, name in ((q, q_out, "q_out"), (None if cache is not None else k, k_out, "k_out")):
-        if t is None:
-            if given is not None:
-                raise ValueError(f"{fn}: {name} without its rows")
-            outs.append(None)
-            strides += (0, 0)
-            ptrs.append(0)
-            continue
-        out = torch.empty(t.shape, dtype=t.dtype, device=t.device) if given is None else given
-        if out.shape != t.shape:
-            raise ValueError(f"{fn}: {name} must be {tuple(t.shape)}, got {tuple(out.shape)}")
-        strides += _rope_rows(fn, out, name, T, x.dtype, dim)
-        ptrs.append(out.data_ptr())
-        outs.append(out)
+        raise ValueError(f"{fn}: rows must be float32, float16 or bfloat16, got {dtype}")
+    q_out = _rope_out(fn, q, q_out, "q_out")
+    if cache is None:
+        k_out = _rope_out(fn, k, k_out, "k_out")
+    none = (0, 0)
+    strides = [none if t is None else _rope_rows(fn, t, name, T, dtype, dim)
+               for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"), (k_out, "k_out"))]
     rot = 0
     if freqs is not None:
         if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
@@ -961,20 +965,20 @@ def _qk_rope(fn, q, k, v, cache, slots, positions, freqs, q_weight, k_weight, ep
             raise ValueError(f"{fn}: positions must be given")
     if positions is not None:
         _int32(fn, positions, (T,), "positions")
-    weights = [w for w in (q_weight, k_weight) if w is not None]
-    for w in weights:
-        if w.dtype not in (x.dtype, torch.float32) or w.dtype != weights[0].dtype or tuple(w.shape) != (dim,) or not w.is_contiguous():
-            raise ValueError(f"{fn}: weights must be contiguous vectors of {dim}, both of {x.dtype} or both float32")
-    _on_device(fn, x if cache is None else cache, q, k, v, *outs, slots, positions, freqs, *weights)
+    w = q_weight if k_weight is None else k_weight
+    for t in (q_weight, k_weight):
+        if t is not None and (t.dtype != w.dtype or t.dtype not in (dtype, torch.float32) or t.shape != (dim,) or not t.is_contiguous()):
+            raise ValueError(f"{fn}: weights must be contiguous vectors of {dim}, both of {dtype} or both float32")
+    _on_device(fn, x if cache is None else cache, q, k, v, q_out, k_out, slots, positions, freqs, q_weight, k_weight)
     if T == 0:
-        return outs
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    args = _QK_ROPE.pack(*ptrs, *strides, ptr(q_weight), ptr(k_weight), ptr(positions), ptr(freqs), ptr(slots), T, eps, weight_offset,
-                         0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim, rot, interleaved, dt,
-                         _TORCH_DT[weights[0].dtype] if weights else dt)
+        return q_out, k_out
+    ptr = [0 if t is None else t.data_ptr() for t in (q, k, v, q_out, k_out, q_weight, k_weight, positions, freqs, slots)]
+    qs, ks, vs, qos, kos = strides
+    args = _QK_ROPE.pack(*ptr[:5], *qs, *ks, *vs, *qos, *kos, *ptr[5:], T, eps, weight_offset, 0 if q is None else q.shape[1],
+                         0 if k is None else k.shape[1], dim, rot, interleaved, dt, dt if w is None else _TORCH_DT[w.dtype])
     s = _raw_stream(x.device.index)
     _check(lib().qk_norm_rope(args, s) if cache is None else lib().kv_cache_write_rope(cache.address, args, s), fn)
-    return outs
+    return q_out, k_out
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None, freqs: torch.Tensor | None, *,
@@ -992,7 +996,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
         return _on_stream(stream, (q, k, positions, freqs, q_weight, k_weight, q_out, k_out),
                           lambda: qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight, eps=eps, weight_offset=weight_offset,
                                                interleaved=interleaved, q_out=q_out, k_out=k_out))
-    return tuple(_qk_rope("qk_norm_rope", q, k, None, None, None, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, k_out))
+    return _qk_rope("qk_norm_rope", q, k, None, None, None, positions, freqs, q_weight, k_weight, eps, weight_offset, interleaved, q_out, k_out)
 
 
 def kv_cache_write_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KVCache, slots: torch.Tensor, positions: torch.Tensor | None,
