@@ -257,3 +257,10 @@ def test_refusals(ops):  # noqa: F811
     t = Case(ops, I8, "bf16", 2, 4, 128, 16, [5], [70], seed=1, tree=True)
     with pytest.raises(TypeError):
         t.run(ops, slopes=torch.zeros(8, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_queries_before_the_sequence(ops, fmt):  # noqa: F811
+    """More queries than positions: those before the first see the prefix alone, or nothing."""
+    both(ops, fmt, "bf16", 2, 4, 128, 16, [9, 70, 3], [4, 20, 0], seed=6, prefix=[2, 0, 5], cap=9.0, slopes=[0.3, 0.02])
+    both(ops, fmt, "f16", 1, 6, 64, 16, [300], [130], seed=6, prefix=[50], window=20, sinks=3, slopes=[0.1])

@@ -219,3 +219,8 @@ def test_scores_are_checked(L):
     big = cache(pages=100000, kv_heads=8)
     long = attn(big, tokens=1, batch=1, max_q=1, cu_q=None, q_heads=32, max_pages=8192)
     assert L.kv_attn_scored(ctypes.addressof(long), ctypes.addressof(Scores(P, None, 0.0)), None, 0, None) == E_WS
+
+
+def test_tree_depths():
+    from bit_gemm_w4_amd.attention_layer import tree_depths
+    assert tree_depths([-1, 0, 0, 2, -1, 4]) == [0, 1, 1, 2, 0, 1] and tree_depths([]) == []
