@@ -28,7 +28,7 @@ namespace bg {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kPhases = 1152;             // cosines and sines of a block; blocks_of keeps to it
+constexpr int kPhases = 1152;             // cosines and sines of a block; grid_of keeps to it
 
 enum { ROW_Q = 0, ROW_K = 1, ROW_V = 2 };
 
@@ -165,21 +165,24 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     const int e0 = halves ? 4 * lane : 8 * lane, e1 = halves ? pairs + 4 * lane : 8 * lane + 4;
     const bool turns = kind != ROW_V && lane < a.rot / 8;
 
-    // row i's token and head, from the block's first
-    struct At {
-        uint32_t t, h;
-    };
-    auto place = [&](uint32_t i) {
-        const uint32_t t = (h0 + i) / (uint32_t)heads;
-        return At{t, h0 + i - t * heads};
-    };
-    uint32_t i = threadIdx.x / L;
+    // The lane's next row: token and head from the block's first, where it lies and where it goes.  SLOTS rows
+    // on is dt tokens and dh heads on, or a token more and the heads less: no division or product a row.
+    constexpr int SIZE = DT == DT_F32 ? 4 : 2;
+    const bool rows_out = kind == ROW_Q || (FMT == 0 && kind == ROW_K);
+    const int64_t ots = kind == ROW_Q ? a.qo_ts : a.ko_ts, ohs = kind == ROW_Q ? a.qo_hs : a.ko_hs;
+    const uint32_t dt = SLOTS / (uint32_t)heads, dh = SLOTS - dt * heads;
+    const int64_t on = (dt * ts + dh * hs) * SIZE, over = (ts - heads * hs) * SIZE;
+    const int64_t out_on = (dt * ots + dh * ohs) * SIZE, out_over = (ots - heads * ohs) * SIZE;
+    uint32_t i = threadIdx.x / L, next_t = (h0 + i) / (uint32_t)heads, next_h = h0 + i - next_t * heads;
+    const char* from = static_cast<const char*>(src) + ((int64_t)(t0 + next_t) * ts + (int64_t)next_h * hs + e0) * SIZE;
+    char* to = static_cast<char*>(kind == ROW_Q ? a.q_out : a.k_out) + ((int64_t)(t0 + next_t) * ots + (int64_t)next_h * ohs + e0) * SIZE;
+    const int apart = (e1 - e0) * SIZE;
     Four<DT> x0{}, x1{};
-    At next = place(i);
+    int64_t next_slot = -1;
     auto ask = [&]() {
-        const int64_t at = (int64_t)(t0 + next.t) * ts + (int64_t)next.h * hs;
-        x0 = load4<DT>(src, at + e0);
-        x1 = load4<DT>(src, at + e1);
+        x0 = load4<DT>(from, 0);
+        x1 = load4<DT>(from + apart, 0);
+        if (FMT != 0 && kind != ROW_Q) next_slot = a.slots[t0 + next_t];
     };
     if (i < rows) ask();
     const void* weight = kind == ROW_Q ? a.q_weight : kind == ROW_K ? a.k_weight : nullptr;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     }
     // pair n of token t: phase[t pairs + (n % 4) pairs / 4 + n / 4], so that lanes read next to each other
     if (kind != ROW_V && pairs > 0 && rows > 0) {
-        const uint32_t some = (place(rows - 1).t + 1) * pairs;
+        const uint32_t some = ((h0 + rows - 1) / (uint32_t)heads + 1) * pairs;
         for (uint32_t n = threadIdx.x; n < some; n += kBlock) {
             const uint32_t t = n / pairs, p = n - t * pairs;
             double c, s;
@@ -210,24 +213,28 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
         float x[8];
         floats4<DT>(x0, x);
         floats4<DT>(x1, x + 4);
-        const uint32_t t = next.t, h = next.h;
+        const uint32_t t = next_t, h = next_h;
+        const int64_t slot = next_slot;
+        char* const here = to;
         if (i + SLOTS < rows) {
-            next = place(i + SLOTS);
+            next_t += dt;
+            next_h += dh;
+            const bool wrap = next_h >= (uint32_t)heads;
+            next_t += wrap ? 1 : 0;
+            next_h -= wrap ? heads : 0;
+            from += wrap ? on + over : on;
+            to += wrap ? out_on + out_over : out_on;
             ask();
         }
-        const uint32_t from = t * pairs + lane;
-        if (!wide && kind != ROW_V) {
-            turn_row<float, D>(a, x, w, weight != nullptr, turns, reinterpret_cast<const float2*>(phase) + from, pairs / 4);
-            void* to = kind == ROW_Q ? a.q_out : a.k_out;
-            const int64_t at = (int64_t)(t0 + t) * (kind == ROW_Q ? a.qo_ts : a.ko_ts) + (int64_t)h * (kind == ROW_Q ? a.qo_hs : a.ko_hs);
-            store4<DT>(to, at + e0, x);
-            store4<DT>(to, at + e1, x + 4);
+        const uint32_t turn = t * pairs + lane;
+        if (rows_out) {
+            turn_row<float, D>(a, x, w, weight != nullptr, turns, reinterpret_cast<const float2*>(phase) + turn, pairs / 4);
+            store4<DT>(here, 0, x);
+            store4<DT>(here + apart, 0, x + 4);
         }
         if constexpr (FMT != 0) {
-            if (kind == ROW_Q) continue;
-            const int64_t slot = a.slots[t0 + t];
-            if (slot < 0 || slot >= (cache.pages << cache.page_shift)) continue;       // whole rows skip together
-            if (wide) turn_row<double, D>(a, x, w, weight != nullptr, turns, phase + from, pairs / 4);
+            if (kind == ROW_Q || slot < 0 || slot >= (cache.pages << cache.page_shift)) continue;       // whole rows skip together
+            if (wide) turn_row<double, D>(a, x, w, weight != nullptr, turns, phase + turn, pairs / 4);
             const int64_t row = kv_row(cache, slot, (int)h);
             uint8_t* codes = (kind == ROW_V ? cache.v : cache.k) + row * (FMT == KV_U4 ? D / 2 : D);
             const RowCodes q = quantize_row<FMT, D>(x);
