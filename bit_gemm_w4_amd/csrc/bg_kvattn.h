@@ -247,14 +247,14 @@ __device__ __forceinline__ RowStep raise_row(float& m, float& fb, float ty, floa
 // The slope of a head's bias, in units of the scores before their last factor, a.cap.  With slopes the
 // tiles are taken from the last one back: a query's nearest positions usually hold its largest scores, so its
 // references seldom move after the first (forwards, in every tile of a steep head: 2,048 queries over a window
-// of 4,096, E4M3, 32 heads of 128, slopes 2^(-i / 4): 395 us, 188 so).
+// of 4,096, E4M3, 32 heads of 128, slopes 2^(-i / 4): 395 us, 171 so).
 __device__ __forceinline__ float head_slope(const KvAttnArgs& a, int head) { return a.slopes[head] * 0x1.715476p0f * (a.cap_inv != 0.0f ? a.cap_inv : 1.0f); }
 
 // Caps up to kCapExp are taken as tanh(u) = 1 - 2 / (1 + 2^x), x = 2 log2(e) u (a factor that the tokens'
 // scales take along): within 2^-21, so a score errs by 2^-21 of its cap, a weight by 2^-13 of itself at most, of
 // which FP16 takes 2^-11.  Larger ones (FAR) as polynomials, within 2^-21 of tanh(u).  Those have fewer vector
 // instructions, 6 a score against what 10 take, but they need their largest score looked at: with a branch
-// on it in the loop the above chunk with a cap of 50 took 288 us, by the power it takes 218.
+// on it in the loop the above chunk with a cap of 50 took 288 us, by the power it takes 211.
 constexpr float kCapExp = 256.0f;
 __device__ __forceinline__ float cap_unit(const KvAttnArgs& a) { return a.cap_far ? a.cap_inv : a.cap_inv * 0x1.715476p1f; }
 

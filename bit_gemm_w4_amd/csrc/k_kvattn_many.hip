@@ -42,6 +42,12 @@
 // references (raise_row in bg_kvattn.h: value scales beyond 2^+-40) takes them so
 // always, too.  A row's largest w s lies at 2^3 at least, so one that falls below
 // FP16's normal range errs by 2^-28 of it.
+//
+// Other scores (k_kvattn_many_*.hip) cost vector instructions, which bound them: the chunk above 176 us as it is
+// with queries of four times the size, 171 with slopes, 211 with a cap of 50, 202 with both, 240 with a cap of 1000.
+// A form each, as what a form does not need costs registers: with caps and slopes behind branches in one kernel 250
+// us (cap) where this takes 211, and at D = 128 value fragments are read two products ahead there, not four (ragged
+// chunks with slopes 193 -> 163 us).
 #include "bg_kvattn_many.h"
 
 namespace bg {
