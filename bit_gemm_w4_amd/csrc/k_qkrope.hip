@@ -18,9 +18,9 @@
 // quantized from there as kv_cache_write does: a code sits next to a border of its rounding, so
 // in binary32 some codes would follow the order of a row's sum.  So they are those of the
 // formula, whatever the split, and they can be tested bit for bit.  Binary64 multiply-adds run
-// at the rate of binary32 ones here; in binary32 the case below would take 11 us less.
+// at the rate of binary32 ones here; in binary32 the case below takes 78 us.
 //
-// 16,383 tokens of 32 query and 8 + 8 key and value heads of 128, BF16 into E4M3: 81 us for
+// 16,383 tokens of 32 query and 8 + 8 key and value heads of 128, BF16 into E4M3: 82 us for
 // 370 MB, 4.6 TB/s (a large copy runs at 5.1); queries alone 45 us, 6.0 TB/s with part of them in the
 // last-level cache; keys and values 33 us, where kv_cache_write takes 27.  First form 105 us: with roots and
 // quotients by the compiler's sequences, a division and 64-bit products for each row, and binary64 copies of rows and
@@ -40,7 +40,7 @@ enum { ROW_Q = 0, ROW_K = 1, ROW_V = 2 };
 
 struct RopeGrid {
     unsigned blocks[3];                   // of queries, keys and values, in this order
-    int rows;                             // of a block
+    int rows[3];                          // of a block
 };
 
 // cos and sin of 2 pi u 2^-64: to the nearest quarter turn, and from there by their series,
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     int kind = ROW_Q;
     for (; kind < ROW_V && block >= grid.blocks[kind]; ++kind) block -= grid.blocks[kind];
     const int heads = kind == ROW_Q ? a.q_heads : a.kv_heads, pairs = a.rot / 2;
-    const uint32_t r0 = block * (uint32_t)grid.rows, all = (uint32_t)a.tokens * heads;
-    const uint32_t rows = all - r0 < (uint32_t)grid.rows ? all - r0 : (uint32_t)grid.rows;
+    const uint32_t per = (uint32_t)grid.rows[kind], r0 = block * per, all = (uint32_t)a.tokens * heads;
+    const uint32_t rows = all - r0 < per ? all - r0 : per;
     const uint32_t t0 = r0 / heads, h0 = r0 - t0 * heads;             // the first row's token and head
     const void* src = kind == ROW_Q ? a.q : kind == ROW_K ? a.k : a.v;
     const int64_t ts = kind == ROW_Q ? a.q_ts : kind == ROW_K ? a.k_ts : a.v_ts, hs = kind == ROW_Q ? a.q_hs : kind == ROW_K ? a.k_hs : a.v_hs;
@@ -253,18 +253,19 @@ __global__ void __launch_bounds__(kBlock) k_qk_rope(RopeArgs a, KvCache cache, R
     }
 }
 
-// Rows of a block: up to eight for each of its row slots while that leaves 2,048 blocks,
-// and no more tokens than their cosines and sines have room in LDS.
+// Rows of a block: up to eight for each of its row slots while that leaves 2,048 blocks, and no more tokens than
+// their cosines and sines have room in LDS.  (So the largest call, 2^28 rows of either, stays below 2^32 threads.)
 RopeGrid grid_of(const RopeArgs& a, int dim, bool cache) {
-    const int slots = kBlock * 8 / dim, pairs = a.rot / 2;
-    const int64_t q = a.tokens * a.q_heads, kv = a.tokens * a.kv_heads, values = cache ? kv : 0;
-    const int fewest = a.q_heads > 0 && a.q_heads < a.kv_heads ? a.q_heads : a.kv_heads > 0 ? a.kv_heads : a.q_heads;
+    const int slots = kBlock * 8 / dim, heads[3] = {a.q_heads, a.kv_heads, cache ? a.kv_heads : 0};
+    const int64_t all = a.tokens * (heads[0] + heads[1] + heads[2]);
     RopeGrid g;
-    int each = 8;
-    while (each > 1 && ((q + kv + values) / (each * slots) < 2048 || ((int64_t)(each * slots - 1) / fewest + 2) * pairs > kPhases)) each /= 2;
-    g.rows = each * slots;
-    const int64_t rows[3] = {q, kv, values};
-    for (int n = 0; n < 3; ++n) g.blocks[n] = (unsigned)((rows[n] + g.rows - 1) / g.rows);
+    for (int n = 0; n < 3; ++n) {
+        const int64_t pairs = n == ROW_V ? 0 : a.rot / 2;
+        int each = heads[n] ? 8 : 1;
+        while (each > 1 && (all / (each * slots) < 2048 || ((each * slots - 1) / heads[n] + 2) * pairs > kPhases)) each /= 2;
+        g.rows[n] = each * slots;
+        g.blocks[n] = (unsigned)((a.tokens * heads[n] + g.rows[n] - 1) / g.rows[n]);
+    }
     return g;
 }
 

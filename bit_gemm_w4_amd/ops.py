@@ -936,6 +936,12 @@ def _rope_out(fn: str, t: torch.Tensor | None, out: torch.Tensor | None, name: s
         return torch.empty(t.shape, dtype=t.dtype, device=t.device)
     if out.shape != t.shape:
         raise ValueError(f"{fn}: {name} must be {tuple(t.shape)}, got {tuple(out.shape)}")
+    # rows that lie in one another would be written at once
+    inner = 1
+    for size, stride in sorted(zip(out.shape, out.stride()), key=lambda x: x[1]):
+        if size > 1 and stride < inner:
+            raise ValueError(f"{fn}: {name}'s rows overlap: strides {tuple(out.stride())}")
+        inner = max(inner, stride * size)
     return out
 
 

@@ -657,9 +657,9 @@ typedef struct bg_kv_pool {
  * none): rows cu_q[b] .. cu_q[b + 1] - 1 of the step, at its positions lens[b]
  * and up.  New pages come off the stack in the order of the sequences, a
  * sequence's pages in their order.  A sequence is served if its rows lie within
- * `tokens`, its positions within the block table, and it needs no page or the
- * pages that it and those before it need (such as have the first two) are there;
- * one that is not gets none, its tokens have no slots and its length stays.
+ * `tokens`, its positions within the block table, and the free pages suffice for it
+ * and all before it that pass these two (or it needs none); one that is not gets
+ * none, its tokens have no slots and its length stays.
  *   cu_q       out [batch + 1], clamped to tokens
  *   kv_lens    out [batch]: the lengths with the new tokens
  *   served     out [batch]: 1 or 0

@@ -90,6 +90,7 @@ CASES = [
     dict(T=70, q_heads=200, kv_heads=3, dim=64, dtype="bf16", rot=64, far=300),      # negative positions too
     dict(T=700, q_heads=16, kv_heads=16, dim=128, dtype="bf16", rot=128),
     dict(T=20, q_heads=4, kv_heads=2, dim=128, dtype="f16", rot=128, fused=False),
+    dict(T=1100, q_heads=64, kv_heads=1, dim=256, dtype="f16", rot=256),          # queries in long runs, keys a slot each
 ]
 
 
@@ -105,6 +106,9 @@ def test_rows(ops, case):
     assert none is None and torch.equal(one, q)
     none, one = ops.qk_norm_rope(None, c.k, c.positions, c.freqs, **c.how)
     assert none is None and torch.equal(one, k)
+    # heads before tokens
+    out = torch.zeros(c.q.shape[1], c.T, c.dim, dtype=c.q.dtype, device="cuda:0").transpose(0, 1)
+    assert torch.equal(ops.qk_norm_rope(c.q, None, c.positions, c.freqs, **c.how, q_out=out)[0], q)
     # in place, in the fused rows
     ops.qk_norm_rope(c.q, c.k, c.positions, c.freqs, **c.how, q_out=c.q, k_out=c.k)
     assert torch.equal(c.q, q) and torch.equal(c.k, k)
@@ -255,6 +259,8 @@ def test_refusals(ops):
         ops.qk_norm_rope(*args, q_weight=c.qw[:64])
     with pytest.raises(ValueError, match="q_out"):
         ops.qk_norm_rope(*args, q_out=c.k)
+    with pytest.raises(ValueError, match="overlap"):
+        ops.qk_norm_rope(*args, q_out=c.q[:, :1].expand(4, 4, 128))
     with pytest.raises(ValueError, match="one device"):
         ops.qk_norm_rope(c.q, c.k, c.positions.cpu(), c.freqs)
     with pytest.raises(ValueError, match="device tensors"):
