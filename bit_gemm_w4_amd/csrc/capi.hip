@@ -11,6 +11,7 @@
 #include "../../include/bitgemm.h"
 #include "bg_internal.h"
 #include "bg_kv.h"
+#include "bg_overlap.h"
 
 #define BG_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -842,6 +843,22 @@ bg_status rope_args(const char* fn, const bg_qk_rope* p, const bg::KvCache* cach
             return fail_in(fn, BG_ERR_ALIGN, "rows and weights must be 16-byte aligned");
         if ((p->rot && (!aligned(p->positions, 4) || !aligned(p->freqs, 8))) || (cache && !aligned(p->slots, 8)))
             return fail_in(fn, BG_ERR_ALIGN, "positions must be 4-byte aligned, freqs and slots 8-byte aligned");
+        // a block writes its rows while others have theirs yet to read
+        const int64_t size = 16 / unit;
+        auto rows = [&](const void* at, int64_t ts, int64_t hs, int n) { return bg::RowSet(at, p->tokens, ts * size, n, hs * size, *dim * size); };
+        const bg::RowSet in[3] = {rows(p->q, p->q_token_stride, p->q_head_stride, p->q_heads), rows(p->k, p->k_token_stride, p->k_head_stride, kv_heads),
+                                  rows(p->v, p->v_token_stride, p->v_head_stride, kv_heads)};
+        const bg::RowSet out[2] = {rows(p->q_out, p->q_out_token_stride, p->q_out_head_stride, p->q_heads),
+                                   rows(p->k_out, p->k_out_token_stride, p->k_out_head_stride, kv_heads)};
+        const bool given[3] = {q, k, cache != nullptr}, written[2] = {q, k_out};
+        for (int o = 0; o < 2; ++o) {
+            if (!written[o]) continue;
+            if (!out[o].distinct()) return fail_in(fn, BG_ERR_UNSUPPORTED, o == 0 ? "q_out's rows overlap" : "k_out's rows overlap");
+            for (int i = 0; i < 3; ++i)
+                if (given[i] && !(i == o && out[o].same(in[i])) && !bg::apart(out[o], in[i]))
+                    return fail_in(fn, BG_ERR_UNSUPPORTED, o == 0 ? "q_out overlaps q (other than as a whole), k or v" : "k_out overlaps k (other than as a whole) or q");
+        }
+        if (written[0] && written[1] && !bg::apart(out[0], out[1])) return fail_in(fn, BG_ERR_UNSUPPORTED, "q_out and k_out overlap");
     }
     *a = bg::RopeArgs{p->q, p->k, p->v, p->q_out, p->k_out, p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
                       p->v_token_stride, p->v_head_stride, p->q_out_token_stride, p->q_out_head_stride, p->k_out_token_stride,

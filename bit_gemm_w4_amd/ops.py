@@ -992,7 +992,8 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
                  interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """Norm each head of queries [T][q_heads][D] and keys [T][kv_heads][D] (either
     may be None) and rotate it by its position (int32 [T]) -> (q, k), new tensors
-    unless q_out / k_out are given (the rows themselves for in place).
+    unless q_out / k_out are given (the rows themselves for in place; otherwise they
+    must not overlap the rows or each other).
 
     x / sqrt(mean(x^2) + eps) * (weight_offset + weight), where a weight [D] is
     given; then the first 2 len(freqs) elements in pairs (n, n + len(freqs)), or with interleaved
@@ -1010,7 +1011,8 @@ def kv_cache_write_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor
                         eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, q_out: torch.Tensor | None = None,
                         stream=None) -> torch.Tensor | None:
     """qk_norm_rope and kv_cache_write in one pass: queries are normed and rotated
-    (-> new tensor, or q_out; None: none), keys too, and go to the cache slots with the values.
+    (-> new tensor, or q_out, which may be the queries and must not overlap the rows otherwise; None: none), keys too, and go to
+    the cache slots with the values.
     Keys are computed in float64 and rounded to float32, from which they are quantized."""
     if stream is not None:
         return _on_stream(stream, (q, k, v, cache.k, cache.v, cache.k_scales, cache.v_scales, slots, positions, freqs, q_weight, k_weight, q_out),

@@ -692,7 +692,9 @@ bg_status kv_release(const bg_kv_pool* pool, const int32_t* keep, void* stream);
  *              x_dtype (F32, F16 or BF16); strides in elements, multiples of 16 bytes.
  *              Either has no heads (q_heads or kv_heads 0) where it is not wanted
  *   q_out, k_out  the same with strides of their own; may be q and k (then with
- *              their strides), and overlap no other input
+ *              their strides), and overlap nothing else (refused where the rows of
+ *              q, k, v or the other output may share memory with them; slices of one
+ *              fused row do not)
  *   q_weight, k_weight  [head_dim] of weight_dtype (x_dtype or F32), or NULL
  *   positions  [tokens], any values
  *   freqs      [rot / 2] turns (of 2 pi) a position in units of 2^-64, so that
