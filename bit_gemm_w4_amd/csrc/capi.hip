@@ -788,6 +788,8 @@ namespace {
 
 constexpr int64_t kMaxPoolPages = int64_t(1) << 30;
 
+bg::Span ints(const void* p, int64_t n) { return bg::Span(p, 4 * (uint64_t)n); }
+
 // The pool of `fn`, checked.
 bg_status kv_pool_of(const char* fn, const bg_kv_pool* p, bg::KvPool* out) {
     if (!p) return fail_in(fn, BG_ERR_NULL, "pool must be non-NULL");
@@ -893,6 +895,20 @@ BG_EXPORT bg_status kv_plan(const bg_kv_pool* pool, const int32_t* q_lens, int64
         return fail_in(fn, BG_ERR_NULL, "q_lens, cu_q, kv_lens, served, positions and slots must be non-NULL");
     if (!aligned(q_lens, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(served, 4) || !aligned(positions, 4) || !aligned(slots, 8))
         return fail_in(fn, BG_ERR_ALIGN, "lengths, offsets and positions must be 4-byte aligned, slots 8-byte aligned");
+    // the first block writes these while others read
+    const bg::Span asked = ints(q_lens, p.batch), out[] = {ints(cu_q, p.batch + 1), ints(kv_lens, p.batch), ints(served, p.batch), ints(positions, tokens),
+                                                           ints(slots, 2 * tokens)};
+    const bg::Span held[] = {ints(p.table, p.batch * p.max_pages), ints(p.free, p.pages), ints(p.state, 2), ints(p.lens, p.batch),
+                             ints(p.gone, p.gone ? p.batch : 0)};
+    for (const bg::Span& x : out) {
+        for (const bg::Span& y : out)
+            if (&x != &y && !bg::apart(x, y)) return fail_in(fn, BG_ERR_UNSUPPORTED, "two outputs overlap");
+        for (const bg::Span& y : held)
+            if (!bg::apart(x, y)) return fail_in(fn, BG_ERR_UNSUPPORTED, "an output overlaps the pool");
+        if (!bg::apart(x, asked)) return fail_in(fn, BG_ERR_UNSUPPORTED, "q_lens overlaps an output");
+    }
+    for (int i = 0; i < 4; ++i)
+        if (!bg::apart(asked, held[i]) && !(i == 3 && q_lens == p.lens)) return fail_in(fn, BG_ERR_UNSUPPORTED, "q_lens overlaps what the step writes of the pool");
     const bg::KvPlan o{q_lens, tokens, advance != 0, cu_q, kv_lens, served, positions, slots};
     note_kernel(bg::launch_kv_plan(p, o, static_cast<hipStream_t>(stream)));
     return launched(fn);
@@ -904,6 +920,10 @@ BG_EXPORT bg_status kv_release(const bg_kv_pool* pool, const int32_t* keep, void
     const bg_status st = kv_pool_of(fn, pool, &p);
     if (st != BG_OK) return st;
     if (!aligned(keep, 4)) return fail_in(fn, BG_ERR_ALIGN, "keep must be 4-byte aligned");
+    if (keep && keep != p.lens && keep != p.gone)           // these are read as they are written, a sequence by one thread
+        for (const bg::Span& y : {ints(p.table, p.batch * p.max_pages), ints(p.free, p.pages), ints(p.state, 2), ints(p.lens, p.batch),
+                                  ints(p.gone, p.gone ? p.batch : 0)})
+            if (!bg::apart(ints(keep, p.batch), y)) return fail_in(fn, BG_ERR_UNSUPPORTED, "keep overlaps the pool");
     note_kernel(bg::launch_kv_release(p, keep, static_cast<hipStream_t>(stream)));
     return launched(fn);
 }

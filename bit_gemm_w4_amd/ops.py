@@ -864,7 +864,7 @@ def kv_plan(pool: KVPool, q_lens: torch.Tensor, tokens: int, *, advance: bool = 
     stays, its rows' slots are -1, and served[b] is 0.  Rows past the last sequence's have slot -1
     and position 0.  advance False: the pool's lengths and free pages stay as they
     are, as for drafts that are yet to be accepted.  out: an earlier plan
-    of the same sizes, to be written over."""
+    of the same sizes, to be written over; q_lens must not be one of its tensors."""
     fn = "kv_plan"
     if stream is not None:
         used = () if out is None else (out.cu_q, out.kv_lens, out.served, out.positions, out.slots)

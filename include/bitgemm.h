@@ -665,6 +665,8 @@ typedef struct bg_kv_pool {
  *   served     out [batch]: 1 or 0
  *   positions  out [tokens]: of each row (of rows past the last sequence's: 0)
  *   slots      out [tokens]: where the row's token goes, -1: nowhere
+ * The outputs must not overlap each other, q_lens or the pool's arrays, nor q_lens
+ * what the step writes of the pool (refused).
  * The block table gets the new pages.  advance != 0: the pool holds the new
  * tokens from now on; 0: lengths and free pages stay, and the entries of the new
  * pages mean nothing after the step (drafts that are yet to be accepted).
@@ -678,7 +680,8 @@ bg_status kv_plan(const bg_kv_pool* pool, const int32_t* q_lens, int64_t tokens,
  * stack; with a window those too that no query at its next position or later sees
  * (keep must not lie in what was given back so before: such positions stay gone).
  * The order is that of kv_plan backwards: a step taken back leaves the stack as
- * it was.  Their block table entries become -1.
+ * it was.  Their block table entries become -1.  keep may be the pool's lens or
+ * gone, and overlap its arrays in no other way (refused).
  */
 bg_status kv_release(const bg_kv_pool* pool, const int32_t* keep, void* stream);
 

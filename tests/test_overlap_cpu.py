@@ -117,3 +117,33 @@ def test_overlapping_outputs_into_the_cache_are_refused(L):  # noqa: F811
     a = fused(x_dtype=F32, weight_dtype=F32, q_out=P + 4 * ROW)
     assert L.kv_cache_write_rope(ctypes.addressof(c), ctypes.addressof(a), None) == E_UNSUP
     assert BF16 != F32
+
+
+def plan_args(**over):
+    """A plan of 3 sequences and 5 rows whose operands lie apart."""
+    a = dict(q_lens=P, cu_q=P + 0x1000, kv_lens=P + 0x2000, served=P + 0x3000, positions=P + 0x4000, slots=P + 0x5000)
+    a.update(over)
+    return [a["q_lens"], 5, 1, a["cu_q"], a["kv_lens"], a["served"], a["positions"], a["slots"]]
+
+
+def apart_pool():
+    from test_kv_steps_cpu import pool
+    return pool(block_table=FAR, lens=FAR + 0x1000, gone=FAR + 0x2000, free_pages=FAR + 0x3000, state=FAR + 0x4000)
+
+
+@pytest.mark.parametrize("over", [
+    dict(q_lens=P + 0x3000), dict(q_lens=P + 0x2000), dict(q_lens=P + 0x1000), dict(q_lens=P + 0x5000 + 36),      # a plan's own output as its input
+    dict(kv_lens=P + 0x3000), dict(cu_q=P + 0x2000 - 12), dict(positions=P + 0x5000 - 16),                       # outputs in one another
+    dict(kv_lens=FAR + 0x1000), dict(served=FAR + 0x2000), dict(slots=FAR + 0x3000), dict(cu_q=FAR + 0x4000), dict(positions=FAR + 44),       # in the pool
+    dict(q_lens=FAR + 0x1000 + 4), dict(q_lens=FAR), dict(q_lens=FAR + 0x3000 - 8), dict(q_lens=FAR + 0x4000 + 4)])
+def test_plans_over_their_own_operands_are_refused(L, over):  # noqa: F811
+    p = apart_pool()
+    assert L.kv_plan(ctypes.addressof(p), *plan_args(**over), None) == E_UNSUP
+    assert L.bg_last_error().decode().startswith("kv_plan: ")
+
+
+@pytest.mark.parametrize("keep", [FAR + 0x1000 + 4, FAR + 0x1000 - 8, FAR + 0x2000 + 8, FAR + 44, FAR + 0x3000, FAR + 0x4000])
+def test_lengths_to_keep_inside_the_pool_are_refused(L, keep):  # noqa: F811
+    p = apart_pool()
+    assert L.kv_release(ctypes.addressof(p), keep, None) == E_UNSUP
+    assert L.bg_last_error().decode().startswith("kv_release: ")
