@@ -93,7 +93,8 @@ __device__ __forceinline__ void attend_many(const KvAttnArgs& a, const KvSplit& 
     const int G = a.q_heads / a.c.heads, rows = own_rows.rows, r0 = own_rows.r0, b = own_rows.b;
     const int last = (rows < r0 + WAVES * kRows ? rows : r0 + WAVES * kRows) - 1;
     const KvRange rg = kv_range<kT, SCORED>(a, q, r0 / G, last / G);
-    const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
+    int t0, t1;
+    kv_run<SCORED>(a, sp, rg, split, t0, t1);
     const int nt = t1 - t0;               // tiles of this block: number i is tile t0 + i of the range
     if (nt <= 0 && split > 0) {          // nothing left for this split
         for (int i = threadIdx.x; i <= last - r0; i += WAVES * 64) {

@@ -101,7 +101,8 @@ __device__ __forceinline__ void attend_few(const KvAttnArgs& a, const KvSplit& s
     const int G = a.q_heads / a.c.heads, rows = own.rows, r0 = own.r0, b = own.b;
     const int last = (rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1;
     const KvRange rg = kv_range<32, SCORED>(a, q, r0 / G, last / G);
-    const int t0 = split * sp.tiles, t1 = split + 1 == sp.splits || t0 + sp.tiles > rg.tiles ? rg.tiles : t0 + sp.tiles;
+    int t0, t1;
+    kv_run<SCORED>(a, sp, rg, split, t0, t1);
     const int32_t* table = a.table + b * a.max_pages;
 
     if (t0 >= t1 && split > 0) {          // nothing left for this split
