@@ -61,8 +61,12 @@ __device__ __forceinline__ uint64_t seen_bits(const KvAttnArgs& a, const KvSeq& 
         const int e = base - q.first;            // bit 0's drafted token
         const uint64_t* w = a.tree + (q.q0 + i) * a.tree_words;
         const int n = e >> 6, sh = e & 63;
-        uint64_t bits = n >= 0 && n < a.tree_words ? w[n] >> sh : 0;
-        if (sh && n + 1 >= 0 && n + 1 < a.tree_words) bits |= w[n + 1] << (64 - sh);
+        // The index in a vector register: as a scalar it became part of 16 words of arguments, which were spilled and
+        // brought back as one, 50 lane moves in each masked tile (16 trees of 64, 4 bits: 161 us, 156 so).
+        int at = n;
+        asm("" : "+v"(at));
+        uint64_t bits = n >= 0 && n < a.tree_words ? w[at] >> sh : 0;
+        if (sh && n + 1 >= 0 && n + 1 < a.tree_words) bits |= w[at + 1] << (64 - sh);
         m |= bits & ~low_bits(-e);
         m &= low_bits(q.kv - base);
     } else {
