@@ -685,6 +685,8 @@ def _kv_attn(fn, q, cache, block_table, kv_lens, cu_q, tree, max_q_len, max_kv_l
         raise ValueError(f"{fn}: slopes must be a contiguous float32 vector of {heads}")
     if prefix_lens is not None:
         _int32(fn, prefix_lens, (B,), "prefix_lens")
+    if 0.0 < abs(softcap) < 1e-30:       # some of these are 0 in binary32: no cap
+        raise ValueError(f"{fn}: softcap {softcap} must be 0 or lie in 1e-30 .. 1e30")
     scored = softcap != 0.0 or slopes is not None or prefix_lens is not None
     if T == 0 or B == 0:
         return out
