@@ -729,7 +729,8 @@ def kv_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens:
     are host-side bounds of the lengths: a sequence's queries past max_q_len are
     left alone, and without it (None) every sequence may own all T, which with
     cu_q costs some speed.  scale None: D ** -0.5.  lse: float32
-    [T][q_heads] that receives the log-sum-exp of the scaled scores.  ws: a
+    [T][q_heads] that receives the log-sum-exp of the scaled scores (capped and biased,
+    where they are).  ws: a
     workspace tensor (kv_attn_workspace_bytes), None for the one cached per stream
     (a captured graph: its own).
 
@@ -863,7 +864,8 @@ def kv_plan(pool: KVPool, q_lens: torch.Tensor, tokens: int, *, advance: bool = 
     pool's block table gets the new pages, off the stack of free ones.  A sequence
     that does not fit (its rows pass `tokens`, its length the block table, or the
     free pages are used up by it and those before it) is not served: its length
-    stays, its rows' slots are -1, and served[b] is 0.  Rows past the last sequence's have slot -1
+    stays, its rows' slots are -1, and served[b] is 0 (kv_attn still takes its rows
+    for queries: their outputs mean nothing).  Rows past the last sequence's have slot -1
     and position 0.  advance False: the pool's lengths and free pages stay as they
     are, as for drafts that are yet to be accepted.  out: an earlier plan
     of the same sizes, to be written over; q_lens must not be one of its tensors."""

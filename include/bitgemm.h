@@ -607,7 +607,7 @@ bg_status kv_attn_tree(const bg_kv_attn* args, void* workspace, int64_t workspac
  * prefix_lens[b] (clamped to 0 .. kv_lens[b]) that lie behind its own, too: j <= own or j <
  * prefix_lens[b], and the window as before.  With a tree softcap only.
  * Computed in binary32 (tanh within 2^-21, for caps beyond 256 2^-21 of its value; distances beyond 2^24 within 2^-23 of theirs).
- * Same workspace as kv_attn / kv_attn_tree.
+ * Same workspace as kv_attn / kv_attn_tree.  lse is of these scores.
  */
 typedef struct bg_kv_scores {
     const float* slopes;
@@ -659,7 +659,8 @@ typedef struct bg_kv_pool {
  * sequence's pages in their order.  A sequence is served if its rows lie within
  * `tokens`, its positions within the block table, and the free pages suffice for it
  * and all before it that pass these two (or it needs none); one that is not gets
- * none, its tokens have no slots and its length stays.
+ * none, its tokens have no slots and its length stays (its rows are still among
+ * cu_q: what attention makes of them means nothing).
  *   cu_q       out [batch + 1], clamped to tokens
  *   kv_lens    out [batch]: the lengths with the new tokens
  *   served     out [batch]: 1 or 0
