@@ -262,9 +262,10 @@ __device__ __forceinline__ RowStep raise_row(float& m, float& fb, float ty, floa
 // tiles are taken from the last one back: a query's nearest positions usually hold its largest scores, so its
 // references seldom move after the first (forwards, in every tile of a steep head: 2,048 queries over a window
 // of 4,096, E4M3, 32 heads of 128, slopes 2^(-i / 4): 395 us, 171 so).
-// It stays finite, as the bias of a query's own position is 0 times it.
+// It stays finite, as the bias of a query's own position is 0 times it; NaN stays NaN.
 __device__ __forceinline__ float head_slope(const KvAttnArgs& a, int head) {
-    return __builtin_amdgcn_fmed3f(a.slopes[head] * 0x1.715476p0f * (a.cap_inv != 0.0f ? a.cap_inv : 1.0f), -0x1.fffffep127f, 0x1.fffffep127f);
+    const float s = a.slopes[head] * 0x1.715476p0f * (a.cap_inv != 0.0f ? a.cap_inv : 1.0f);
+    return __builtin_fabsf(s) == __builtin_inff() ? __builtin_copysignf(0x1.fffffep127f, s) : s;
 }
 
 // Caps up to kCapExp are taken as tanh(u) = 1 - 2 / (1 + 2^x), x = 2 log2(e) u (a factor that the tokens'

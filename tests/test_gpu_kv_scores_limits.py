@@ -51,3 +51,14 @@ def test_slopes_that_leave_a_query_its_own_position(ops, fmt, how, slope):  # no
             tol = (u + 2.0 ** -11) * (1 + u) * np.abs(own) + 2.0 ** -24
             assert (np.abs(got[first:first + n, :2] - own[:, None]) <= tol[:, None]).all(), (b, n)
             first += n
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("cap", [0.0, 20.0, 500.0])
+def test_a_slope_of_nan_is_seen_in_its_head_alone(ops, fmt, cap):  # noqa: F811
+    for s in (Scored(ops, fmt, "f16", 1, 3, 64, 16, [1, 1, 30], [1, 300, 40], cap=cap, slopes=[0.1, 0.1, 0.25]),
+              Many(ops, fmt, 64, 32, group=2, cap=cap, slopes=[0.1, 0.01])):
+        want = s.run(ops)
+        s.how["slopes"][1] = float("nan")
+        got = s.run(ops)
+        assert torch.isnan(got[:, 1]).all() and torch.isfinite(got[:, 0]).all() and torch.equal(got[:, 0], want[:, 0])
